@@ -332,6 +332,110 @@ W4A_API int w4a_attn_prefill(const uint16_t* q, const uint16_t* k_cache, const u
                      int start_pos, int T, const uint16_t* k_new, const uint16_t* v_new, uint16_t* out,
                      void* ws, size_t ws_bytes, void* stream);
 
+/* ---- paged KV cache ---------------------------------------------------------
+ * A cache of pages for a batch whose sequences share a prefix (a system
+ * prompt, a document): the prefix's pages are held once and read once for the
+ * whole batch.  The model card motivates its 3:1 sliding-window stack by the
+ * KV bytes of serving ("Why the 3:1 SWA layout matters for serving"); the
+ * pages have no counterpart of these entry points.
+ *
+ * Layer l stores K then V, each [n_pages][n_kv_heads][page_size][head_dim]
+ * bf16, rows in plain order; a page id means the same page in every layer, and
+ * sliding-window layers keep every position (the window is a mask).
+ * page_size: a power of two, 16 .. 256.  n_pages * page_size and n_pages *
+ * n_kv_heads below 2^31.
+ * The batch's sequences (at most 4,096 a call) share `prefix_len` positions,
+ * kept in the pages prefix_table[0 .. ceil(prefix_len / page_size)).  Sequence
+ * b's own positions follow: own position i, position prefix_len + i, is row
+ * i % page_size of page table[b][i / page_size]; lens[b] counts them.  A
+ * prefix is itself filled as a sequence of a call with prefix_len 0: its table
+ * row is then the prefix table of the others.
+ * One step is w4a_paged_plan, then for every layer w4a_qk_prep_paged and
+ * w4a_attn_shared, on one stream; nothing is read back by the host, so a step
+ * can be captured into a CUDA graph. */
+W4A_API int w4a_paged_kv_bytes(const W4AConfig* cfg, int n_pages, int page_size, size_t* bytes);
+/* Byte offsets of layer l's K and V pages. */
+W4A_API int w4a_paged_kv_layer(const W4AConfig* cfg, int n_pages, int page_size, int layer, size_t* k_offset,
+                       size_t* v_offset);
+
+/* Block tables and slot maps of one step.  n_new[b] >= 0: that many new tokens
+ * join sequence b, whose own length is lens[b] so far; n_new[b] = -1: the
+ * sequence ends and its pages return to the queue.  The free pages are a
+ * circular queue of n_queue entries (n_queue = the cache's pages), state =
+ * {head, count}: entries queue[(head + i) % n_queue], i < count.
+ *   Ended sequences append their pages to the queue (by sequence, then by
+ *   page); then the others take the pages that their new positions need from
+ *   its head, by sequence: table[b][ceil(lens[b] / page_size) + j].
+ *   lens_out[b] = lens[b] + n_new[b], 0 for an ended sequence.
+ *   state_out = the queue's new head and count.
+ *   row_start[b], b <= batch: exclusive sums of the new tokens.
+ *   Row r = row_start[b] + i: pos[r] = prefix_len + lens[b] + i, slots[r] =
+ *   page * page_size + row of that position; rows from row_start[batch] to
+ *   max_rows are -1 in both.
+ * All device int32: n_new, lens, lens_out [batch]; state, state_out [2];
+ * queue [n_queue] and table [batch][table_width] updated in place; row_start
+ * [batch + 1]; slots, pos [max_rows].  The outputs must not overlap the inputs
+ * (lens_out and state_out are other buffers: a step that failed, or a graph
+ * replay, can start again from the old ones); entries of table past a
+ * sequence's pages are left as they are.
+ * All or nothing: when pages, table width or max_rows do not suffice, or an
+ * input is out of range, nothing is taken or returned, lens_out = lens,
+ * state_out = state, there are no rows, and w4a_check reports W4A_ERR_KERNEL.
+ * The sequences' pages and the queue must be disjoint; that is not checked.
+ * A page id outside [0, n_queue) is reported, and its rows get slot -1.
+ * ws: >= 256 device bytes, zeroed once (error word). */
+W4A_API int w4a_paged_plan(const int32_t* n_new, const int32_t* lens, const int32_t* state, int32_t* queue, int n_queue,
+                   int32_t* table, int batch, int table_width, int page_size, int prefix_len, int32_t* lens_out,
+                   int32_t* state_out, int32_t* row_start, int32_t* slots, int32_t* pos, int max_rows, void* ws,
+                   size_t ws_bytes, void* stream);
+
+/* w4a_qk_prep for the rows of a step and the paged cache: qkv fp32 [rows]
+ * [q_dim + 2 kv_dim] with `ld` floats between rows (a multiple of 4; the QKV
+ * product as w4a_gemv and w4a_gemm write it has ld = q_dim + 2 kv_dim).
+ * q_out bf16 [rows, n_heads, head_dim] = rope(RMSNorm(q) * q_gain) at
+ * pos[r]; rope(RMSNorm(k) * k_gain) and v go to slot slots[r] of k_pages /
+ * v_pages (one layer's).  A row with slot -1 is skipped: nothing of it is read
+ * or written, its q_out row included.  Two rows must not have one slot.  A
+ * slot outside the cache, or a negative position, is skipped and reported by
+ * w4a_check.  The angle is formed in fp64, so far positions keep their phase.
+ * Of cfg n_heads, n_kv_heads, head_dim, eps and the rotation's fields are
+ * used; (n_heads + 2 n_kv_heads) * head_dim <= 51,200.  qkv, q_out, the gains
+ * and the pages 16-byte aligned.  ws as for w4a_paged_plan. */
+W4A_API int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, int64_t ld, int rows, const float* q_gain,
+                      const float* k_gain, const int32_t* pos, const int32_t* slots, uint16_t* q_out,
+                      uint16_t* k_pages, uint16_t* v_pages, int n_pages, int page_size, void* ws, size_t ws_bytes,
+                      void* stream);
+
+/* Attention of a step's rows over one layer's pages: row r = row_start[b] + i
+ * of sequence b, whose n = row_start[b + 1] - row_start[b] rows are the last
+ * of its lens[b] own positions (lens after the step's append, the plan's
+ * lens_out), is at position p = prefix_len + lens[b] - n + i and sees the
+ * positions j <= p, with window > 0 only those with p - j < window; the
+ * prefix's from prefix_table, read once for the batch, its own from table[b].
+ * out[r] bf16 [n_heads, head_dim] = softmax(q k / sqrt(head_dim)) v, query head
+ * h over KV head h / (n_heads / n_kv_heads).
+ * q, out: bf16 [rows, n_heads, head_dim]; rows from row_start[batch] on are
+ * neither read nor written.  head_dim 64 or 128, at most 16 query heads per KV
+ * head, at most 2^20 rows.  max_new: no sequence has more rows than this (it
+ * sizes the work; 1 for a decode step).  prefix_table may be NULL when
+ * prefix_len is 0.  Positions that no row of a sequence sees (the unwritten
+ * rest of a page, keys before the window) never reach its outputs, whatever
+ * the pages hold there.
+ * A sequence whose numbers do not fit (n > max_new, n > lens[b], lens[b] beyond
+ * the table, rows outside [0, rows]) is skipped, a page id outside the cache
+ * makes the outputs that read it meaningless; both are reported by w4a_check.
+ * Softmax statistics and sums in fp32, in a fixed order: results are
+ * bit-reproducible.
+ * ws: device scratch of w4a_attn_shared_workspace_bytes() bytes, its first 256
+ * zeroed once (error word); not shared by calls that overlap in time. */
+W4A_API int w4a_attn_shared_workspace_bytes(int rows, int batch, int n_heads, int n_kv_heads, int head_dim, int max_new,
+                                    size_t* bytes);
+W4A_API int w4a_attn_shared(const uint16_t* q, int rows, int batch, int n_heads, int n_kv_heads, int head_dim,
+                    const uint16_t* k_pages, const uint16_t* v_pages, int n_pages, int page_size,
+                    const int32_t* row_start, const int32_t* lens, const int32_t* table, int table_width,
+                    const int32_t* prefix_table, int prefix_len, int window, int max_new, uint16_t* out, void* ws,
+                    size_t ws_bytes, void* stream);
+
 /* Profiling aid (off by default).  With a device buffer set, every later
  * w4a_decode_step / w4a_prefill launch writes, per phase p (5 per layer, then
  * lm_head and argmax) and CTA c, eight %globaltimer stamps (ns) as uint64 at

@@ -89,6 +89,12 @@ PROTOTYPES = {
     "w4a_gemm_workspace_bytes": (_I, [C.POINTER(W4ATensor), _SZP]),
     "w4a_gemm": (_I, [C.POINTER(W4ATensor), _P, _I, _P, _P, _I, _P, _SZ, _P]),
     "w4a_attn_prefill": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _SZ, _P]),
+    "w4a_paged_kv_bytes": (_I, [C.POINTER(W4AConfig), _I, _I, _SZP]),
+    "w4a_paged_kv_layer": (_I, [C.POINTER(W4AConfig), _I, _I, _I, _SZP, _SZP]),
+    "w4a_paged_plan": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _I, _P, _SZ, _P]),
+    "w4a_qk_prep_paged": (_I, [C.POINTER(W4AConfig), _I, _P, _I64, _I, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _SZ, _P]),
+    "w4a_attn_shared_workspace_bytes": (_I, [_I, _I, _I, _I, _I, _I, _SZP]),
+    "w4a_attn_shared": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P, _P, _P, _I, _P, _I, _I, _I, _P, _P, _SZ, _P]),
     "w4a_trace": (_I, [_P, _SZ]),
     "w4a_check": (_I, [_P, _SZ, _P]),
     "w4a_sample_workspace_bytes": (_I, [_I, _I, C.POINTER(C.c_size_t)]),

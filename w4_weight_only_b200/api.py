@@ -7,7 +7,7 @@ outputs.  All arithmetic runs in the library's CUDA kernels.
 from __future__ import annotations
 
 import ctypes as C
-from typing import Dict, List, Optional, Sequence
+from typing import Dict, List, NamedTuple, Optional, Sequence
 
 import torch
 
@@ -495,6 +495,168 @@ def attn_prefill(q: torch.Tensor, k_region: torch.Tensor, v_region: torch.Tensor
         out = torch.empty((T, nq, hd), dtype=torch.float16, device=q.device)
     call("w4a_attn_prefill", _p(q), _p(k_region), _p(v_region), batch, seq, nq, n_kv, hd, slots, window,
          start_pos, T, _p(k_new), _p(v_new), _p(out), _p(ws), ws.numel(), _stream())
+    return out
+
+
+# ---------------------------------------------------------------------------
+# paged KV cache, attention behind a shared prefix
+# ---------------------------------------------------------------------------
+def _together(first: torch.Tensor, **others: Optional[torch.Tensor]) -> torch.cuda.device:
+    """Every tensor on the first one's device, which the call then runs on (on
+    that device's current stream)."""
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name}: expected a tensor on {first.device}, got {t.device}")
+    return torch.cuda.device(first.device)
+
+
+def _shaped(t: torch.Tensor, dtype: torch.dtype, name: str, *shape):
+    _need(t, dtype, name)
+    if len(t.shape) != len(shape) or any(s is not None and s != d for s, d in zip(shape, t.shape)):
+        raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+
+
+class PagedKVCache:
+    """One zero-filled device allocation of pages, K and V of every layer
+    (w4a_paged_kv_bytes)."""
+
+    def __init__(self, cfg: Config, n_pages: int, page_size: int = 64, device=None):
+        self.cfg, self.n_pages, self.page_size = cfg, n_pages, page_size
+        c = cfg.to_c()
+        nbytes = _size_out("w4a_paged_kv_bytes", C.byref(c), n_pages, page_size)
+        self.mem = torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
+        self.offsets = []
+        for l in range(cfg.n_layers):
+            ko, vo = C.c_size_t(0), C.c_size_t(0)
+            call("w4a_paged_kv_layer", C.byref(c), n_pages, page_size, l, C.byref(ko), C.byref(vo))
+            self.offsets.append((ko.value, vo.value))
+
+    def layer_views(self, layer: int):
+        """(K, V) as bf16 tensors [n_pages, n_kv, page_size, hd]."""
+        cfg = self.cfg
+        shape = (self.n_pages, cfg.n_kv_heads, self.page_size, cfg.head_dim)
+        n = 2 * self.n_pages * cfg.n_kv_heads * self.page_size * cfg.head_dim
+        return tuple(self.mem[o:o + n].view(torch.bfloat16).view(shape) for o in self.offsets[layer])
+
+    def free_queue(self):
+        """(queue, state) int32: every page free, in order."""
+        dev = self.mem.device
+        return (torch.arange(self.n_pages, dtype=torch.int32, device=dev),
+                torch.tensor([0, self.n_pages], dtype=torch.int32, device=dev))
+
+
+class PagedPlan(NamedTuple):
+    """What w4a_paged_plan writes: the sequences' new own lengths [B], the free
+    queue's state [2], row_start [B + 1], slots and positions [max_rows]."""
+    lens: torch.Tensor
+    state: torch.Tensor
+    row_start: torch.Tensor
+    slots: torch.Tensor
+    pos: torch.Tensor
+
+
+def paged_plan(n_new: torch.Tensor, lens: torch.Tensor, state: torch.Tensor, queue: torch.Tensor, table: torch.Tensor,
+               page_size: int, max_rows: int, prefix_len: int = 0, ws: Optional[torch.Tensor] = None,
+               out: Optional[PagedPlan] = None) -> PagedPlan:
+    """Block tables and slot maps of one step (w4a_paged_plan): n_new int32 [B]
+    new tokens of each sequence (-1 ends it), lens [B] own positions so far,
+    the free queue [n_pages] with its state {head, count}; queue and table
+    [B, width] are updated in place.  check(ws) raises if pages, table width or
+    rows did not suffice (nothing has changed then)."""
+    B = n_new.numel()
+    _shaped(n_new, torch.int32, "n_new", None)
+    _shaped(lens, torch.int32, "lens", B)
+    _shaped(state, torch.int32, "state", 2)
+    _shaped(queue, torch.int32, "queue", None)
+    _shaped(table, torch.int32, "table", B, None)
+    dev = n_new.device
+    if out is None:
+        out = PagedPlan(*(torch.empty((n,), dtype=torch.int32, device=dev)
+                          for n in (B, 2, B + 1, max_rows, max_rows)))
+    else:
+        for name, n in zip(PagedPlan._fields, (B, 2, B + 1, max_rows, max_rows)):
+            _shaped(getattr(out, name), torch.int32, "out." + name, n)
+    if ws is None:
+        ws = zeros_workspace(256, dev)
+    with _together(n_new, lens=lens, state=state, queue=queue, table=table, ws=ws, out_lens=out.lens,
+                   out_state=out.state, row_start=out.row_start, slots=out.slots, pos=out.pos):
+        call("w4a_paged_plan", _p(n_new), _p(lens), _p(state), _p(queue), queue.numel(), _p(table), B, table.shape[1],
+             page_size, prefix_len, _p(out.lens), _p(out.state), _p(out.row_start), _p(out.slots), _p(out.pos),
+             max_rows, _p(ws), ws.numel(), _stream())
+    return out
+
+
+def qk_prep_paged(cfg: Config, full: bool, qkv: torch.Tensor, q_gain: torch.Tensor, k_gain: torch.Tensor,
+                  pos: torch.Tensor, slots: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                  ws: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """QK-norm, rotation and append of a step's rows (w4a_qk_prep_paged): qkv
+    fp32 [rows, q_dim + 2 kv_dim] (rows may be strided), pos and slots int32
+    [rows] from paged_plan (rows with slot -1 are skipped); returns q bf16
+    [rows, n_heads, hd]."""
+    if qkv.dtype != torch.float32:
+        raise TypeError(f"qkv: expected {torch.float32}, got {qkv.dtype}")
+    if qkv.dim() != 2 or qkv.shape[1] != cfg.qkv_dim or qkv.stride(1) != 1:
+        raise ValueError(f"qkv: expected [rows, {cfg.qkv_dim}] with contiguous rows")
+    R = qkv.shape[0]
+    _shaped(q_gain, torch.float32, "q_gain", cfg.q_dim)
+    _shaped(k_gain, torch.float32, "k_gain", cfg.kv_dim)
+    _shaped(pos, torch.int32, "pos", R)
+    _shaped(slots, torch.int32, "slots", R)
+    _shaped(k_pages, torch.bfloat16, "k_pages", None, cfg.n_kv_heads, None, cfg.head_dim)
+    _shaped(v_pages, torch.bfloat16, "v_pages", *k_pages.shape)
+    if q_out is None:
+        q_out = torch.empty((R, cfg.n_heads, cfg.head_dim), dtype=torch.bfloat16, device=qkv.device)
+    _shaped(q_out, torch.bfloat16, "q_out", R, cfg.n_heads, cfg.head_dim)
+    if ws is None:
+        ws = zeros_workspace(256, qkv.device)
+    c = cfg.to_c()
+    with _together(qkv, q_gain=q_gain, k_gain=k_gain, pos=pos, slots=slots, k_pages=k_pages, v_pages=v_pages, ws=ws,
+                   q_out=q_out):
+        call("w4a_qk_prep_paged", C.byref(c), 1 if full else 0, _p(qkv), qkv.stride(0), R, _p(q_gain), _p(k_gain),
+             _p(pos), _p(slots), _p(q_out), _p(k_pages), _p(v_pages), k_pages.shape[0], k_pages.shape[2], _p(ws),
+             ws.numel(), _stream())
+    return q_out
+
+
+def attn_shared_workspace(rows: int, batch: int, n_heads: int, n_kv_heads: int, head_dim: int, max_new: int = 1,
+                          device=None) -> torch.Tensor:
+    return zeros_workspace(_size_out("w4a_attn_shared_workspace_bytes", rows, batch, n_heads, n_kv_heads, head_dim,
+                                     max_new), device)
+
+
+def attn_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, row_start: torch.Tensor,
+                lens: torch.Tensor, table: torch.Tensor, prefix_table: Optional[torch.Tensor] = None,
+                prefix_len: int = 0, window: int = 0, max_new: int = 1, ws: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Attention of a step's rows q bf16 [rows, n_heads, hd] over one layer's
+    pages [n_pages, n_kv, page_size, hd] (w4a_attn_shared): row_start [B + 1]
+    and lens [B] from paged_plan, table [B, width]; the first prefix_len
+    positions of every sequence in the pages prefix_table, read once for the
+    batch.  max_new: the most rows a sequence has.  Returns bf16 [rows,
+    n_heads, hd]; rows behind the last sequence are left as they were."""
+    _shaped(q, torch.bfloat16, "q", None, None, None)
+    R, nq, hd = q.shape
+    _shaped(k_pages, torch.bfloat16, "k_pages", None, None, None, hd)
+    _shaped(v_pages, torch.bfloat16, "v_pages", *k_pages.shape)
+    n_pages, nkv, page = k_pages.shape[:3]
+    B = lens.numel()
+    _shaped(lens, torch.int32, "lens", None)
+    _shaped(row_start, torch.int32, "row_start", B + 1)
+    _shaped(table, torch.int32, "table", B, None)
+    if prefix_table is not None:
+        _shaped(prefix_table, torch.int32, "prefix_table", None)
+        if prefix_table.numel() * page < prefix_len:
+            raise ValueError(f"prefix_table: {prefix_table.numel()} pages hold no {prefix_len} positions")
+    if ws is None:
+        ws = attn_shared_workspace(R, B, nq, nkv, hd, max_new, q.device)
+    if out is None:
+        out = torch.empty_like(q)
+    _shaped(out, torch.bfloat16, "out", R, nq, hd)
+    with _together(q, k_pages=k_pages, v_pages=v_pages, row_start=row_start, lens=lens, table=table,
+                   prefix_table=prefix_table, ws=ws, out=out):
+        call("w4a_attn_shared", _p(q), R, B, nq, nkv, hd, _p(k_pages), _p(v_pages), n_pages, page, _p(row_start),
+             _p(lens), _p(table), table.shape[1], _p(prefix_table), prefix_len, window, max_new, _p(out), _p(ws),
+             ws.numel(), _stream())
     return out
 
 

@@ -40,6 +40,15 @@ cudaError_t launch_final_row(const float*, const float*, int, float, uint16_t*, 
 cudaError_t launch_head_gemv(const uint8_t*, int, int, const uint16_t*, float*, int*, int, cudaStream_t);
 cudaError_t launch_qk_rows(const float*, const float*, const float*, uint16_t*, uint16_t*, uint16_t*, const double*,
                            float, float, int, int, int, int, int, cudaStream_t);
+cudaError_t launch_paged_plan(const int32_t*, const int32_t*, const int32_t*, int32_t*, int32_t*, int32_t*, int32_t*,
+                              int32_t*, int32_t*, int32_t*, uint32_t*, int, int, int, int, int, int, cudaStream_t);
+cudaError_t launch_prep_paged(const float*, int64_t, const float*, const float*, const int32_t*, const int32_t*, int,
+                              uint16_t*, uint16_t*, uint16_t*, uint32_t*, const double*, float, float, int, int, int,
+                              int, int, cudaStream_t);
+cudaError_t launch_attn_shared(const uint16_t*, int, int, int, int, int, const uint16_t*, const uint16_t*, int, int,
+                               const int32_t*, const int32_t*, const int32_t*, int, const int32_t*, int, int, int,
+                               uint16_t*, uint8_t*, int, cudaStream_t);
+size_t attn_shared_ws(int, int, int, int, int, int, int);
 }  // namespace w4a
 
 using namespace w4a;
@@ -1119,6 +1128,171 @@ int w4a_attn_prefill(const uint16_t* q, const uint16_t* k_cache, const uint16_t*
   return W4A_OK;
 }
 
+// ---- paged KV cache -----------------------------------------------------------------
+static int check_pages(int n_pages, int page_size, int n_kv_heads) {
+  if (page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+    return fail(W4A_ERR_SHAPE, "page_size %d (a power of two, 16..256)", page_size);
+  if (n_pages < 1 || (long long)n_pages * page_size > 0x7fffffffLL || (long long)n_pages * n_kv_heads > 0x7fffffffLL)
+    return fail(W4A_ERR_SHAPE, "n_pages %d", n_pages);
+  return W4A_OK;
+}
+
+// Heads of the paged cache's entry points: wider than the engine's, which
+// packs at most MAX_GQ query heads per KV head.
+static int check_paged_heads(int nq, int nkv, int hd) {
+  if (hd != 64 && hd != 128) return fail(W4A_ERR_UNSUPPORTED, "head_dim %d", hd);
+  if (nkv < 1 || nq < 1 || nq % nkv || nq / nkv > MAX_PAGED_GQ || nq > 1024)
+    return fail(W4A_ERR_SHAPE, "heads %d / kv heads %d", nq, nkv);
+  return W4A_OK;
+}
+
+static bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return an && bn && x < y + bn && y < x + an;
+}
+
+int w4a_paged_kv_bytes(const W4AConfig* cfg, int n_pages, int page_size, size_t* bytes) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  if (!bytes) return fail(W4A_ERR_ARG, "null output");
+  rc = check_pages(n_pages, page_size, cfg->n_kv_heads);
+  if (rc) return rc;
+  *bytes = (size_t)2 * cfg->n_layers * n_pages * cfg->n_kv_heads * page_size * cfg->head_dim * 2;
+  return W4A_OK;
+}
+
+int w4a_paged_kv_layer(const W4AConfig* cfg, int n_pages, int page_size, int layer, size_t* k_offset,
+                       size_t* v_offset) {
+  int rc = check_config(cfg);
+  if (rc) return rc;
+  rc = check_pages(n_pages, page_size, cfg->n_kv_heads);
+  if (rc) return rc;
+  if (layer < 0 || layer >= cfg->n_layers) return fail(W4A_ERR_ARG, "layer %d", layer);
+  // a multiple of 16 rows of 128 bytes: every region starts on a 2 KB boundary
+  const size_t one = (size_t)n_pages * cfg->n_kv_heads * page_size * cfg->head_dim * 2;
+  if (k_offset) *k_offset = 2 * layer * one;
+  if (v_offset) *v_offset = (2 * layer + 1) * one;
+  return W4A_OK;
+}
+
+int w4a_paged_plan(const int32_t* n_new, const int32_t* lens, const int32_t* state, int32_t* queue, int n_queue,
+                   int32_t* table, int batch, int table_width, int page_size, int prefix_len, int32_t* lens_out,
+                   int32_t* state_out, int32_t* row_start, int32_t* slots, int32_t* pos, int max_rows, void* ws,
+                   size_t ws_bytes, void* stream) {
+  if (!n_new || !lens || !state || !queue || !table || !lens_out || !state_out || !row_start || !ws)
+    return fail(W4A_ERR_ARG, "null pointer");
+  if (max_rows < 0) return fail(W4A_ERR_SHAPE, "max_rows %d", max_rows);
+  if (max_rows > 0 && (!slots || !pos)) return fail(W4A_ERR_ARG, "null pointer");
+  if (batch < 1 || batch > MAX_PAGED_BATCH) return fail(W4A_ERR_SHAPE, "batch %d (1..%d)", batch, MAX_PAGED_BATCH);
+  if (table_width < 1 || prefix_len < 0) return fail(W4A_ERR_SHAPE, "table_width %d prefix_len %d", table_width, prefix_len);
+  int rc = check_pages(n_queue, page_size, 1);
+  if (rc) return rc;
+  const struct {
+    const void* p;
+    size_t n;
+  } in[3] = {{n_new, (size_t)batch * 4}, {lens, (size_t)batch * 4}, {state, 8}},
+    out[7] = {{queue, (size_t)n_queue * 4},
+              {table, (size_t)batch * table_width * 4},
+              {lens_out, (size_t)batch * 4},
+              {state_out, 8},
+              {row_start, (size_t)(batch + 1) * 4},
+              {slots, (size_t)max_rows * 4},
+              {pos, (size_t)max_rows * 4}};
+  for (int o = 0; o < 7; ++o) {
+    for (int i = 0; i < 3; ++i)
+      if (overlap(in[i].p, in[i].n, out[o].p, out[o].n)) return fail(W4A_ERR_ARG, "an output overlaps an input");
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[i].p, out[i].n, out[o].p, out[o].n)) return fail(W4A_ERR_ARG, "two outputs overlap");
+  }
+  if (!aligned16(ws)) return fail(W4A_ERR_ALIGN, "workspace not 16-byte aligned");
+  if (ws_bytes < 256) return fail(W4A_ERR_WORKSPACE, "workspace %zu < 256 bytes", ws_bytes);
+  CK(launch_paged_plan(n_new, lens, state, queue, table, lens_out, state_out, row_start, slots, pos,
+                       static_cast<uint32_t*>(ws) + 2, batch, n_queue, table_width, page_size, prefix_len, max_rows,
+                       S(stream)));
+  return W4A_OK;
+}
+
+int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, int64_t ld, int rows, const float* q_gain,
+                      const float* k_gain, const int32_t* pos, const int32_t* slots, uint16_t* q_out,
+                      uint16_t* k_pages, uint16_t* v_pages, int n_pages, int page_size, void* ws, size_t ws_bytes,
+                      void* stream) {
+  if (!cfg || !qkv || !q_gain || !k_gain || !pos || !slots || !q_out || !k_pages || !v_pages || !ws)
+    return fail(W4A_ERR_ARG, "null pointer");
+  const int nq = cfg->n_heads, nkv = cfg->n_kv_heads, hd = cfg->head_dim;
+  int rc = check_paged_heads(nq, nkv, hd);
+  if (rc) return rc;
+  rc = check_pages(n_pages, page_size, nkv);
+  if (rc) return rc;
+  const int width = (nq + 2 * nkv) * hd;
+  if (width > 51200) return fail(W4A_ERR_SHAPE, "a QKV row of %d values (at most 51200)", width);
+  if (rows < 1) return fail(W4A_ERR_SHAPE, "rows %d", rows);
+  if (ld < width || ld % 4) return fail(W4A_ERR_SHAPE, "row stride %lld (at least %d, a multiple of 4)", (long long)ld, width);
+  if (!aligned16(qkv) || !aligned16(q_gain) || !aligned16(k_gain) || !aligned16(q_out) || !aligned16(k_pages) ||
+      !aligned16(v_pages) || !aligned16(ws))
+    return fail(W4A_ERR_ALIGN, "misaligned pointer");
+  if (ws_bytes < 256) return fail(W4A_ERR_WORKSPACE, "workspace %zu < 256 bytes", ws_bytes);
+  double tab[2][64];
+  float ms[2];
+  rope_tables(cfg, tab, ms);
+  const int t = full ? 1 : 0;
+  CK(launch_prep_paged(qkv, ld, q_gain, k_gain, pos, slots, rows, q_out, k_pages, v_pages,
+                       static_cast<uint32_t*>(ws) + 2, tab[t], ms[t], float(cfg->eps), nq, nkv, hd, n_pages, page_size,
+                       S(stream)));
+  return W4A_OK;
+}
+
+static int check_shared(int rows, int batch, int nq, int nkv, int hd, int max_new) {
+  const int rc = check_paged_heads(nq, nkv, hd);
+  if (rc) return rc;
+  if (batch < 1 || batch > MAX_PAGED_BATCH) return fail(W4A_ERR_SHAPE, "batch %d (1..%d)", batch, MAX_PAGED_BATCH);
+  if (rows < 1 || rows > (1 << 20)) return fail(W4A_ERR_SHAPE, "rows %d (1..2^20)", rows);
+  if (max_new < 1) return fail(W4A_ERR_SHAPE, "max_new %d", max_new);
+  return W4A_OK;
+}
+
+int w4a_attn_shared_workspace_bytes(int rows, int batch, int n_heads, int n_kv_heads, int head_dim, int max_new,
+                                    size_t* bytes) {
+  if (!bytes) return fail(W4A_ERR_ARG, "null output");
+  int rc = check_shared(rows, batch, n_heads, n_kv_heads, head_dim, max_new);
+  if (rc) return rc;
+  int nc;
+  rc = nc_for_sizing(&nc);
+  if (rc) return rc;
+  *bytes = attn_shared_ws(rows, batch, n_heads, n_kv_heads, head_dim, max_new, nc);
+  return W4A_OK;
+}
+
+int w4a_attn_shared(const uint16_t* q, int rows, int batch, int n_heads, int n_kv_heads, int head_dim,
+                    const uint16_t* k_pages, const uint16_t* v_pages, int n_pages, int page_size,
+                    const int32_t* row_start, const int32_t* lens, const int32_t* table, int table_width,
+                    const int32_t* prefix_table, int prefix_len, int window, int max_new, uint16_t* out, void* ws,
+                    size_t ws_bytes, void* stream) {
+  if (!q || !k_pages || !v_pages || !row_start || !lens || !table || !out || !ws)
+    return fail(W4A_ERR_ARG, "null pointer");
+  int rc = check_shared(rows, batch, n_heads, n_kv_heads, head_dim, max_new);
+  if (rc) return rc;
+  rc = check_pages(n_pages, page_size, n_kv_heads);
+  if (rc) return rc;
+  if (prefix_len < 0 || prefix_len > (1 << 30)) return fail(W4A_ERR_SHAPE, "prefix_len %d (0..2^30)", prefix_len);
+  if (prefix_len > 0 && !prefix_table) return fail(W4A_ERR_ARG, "null prefix_table");
+  if (window < 0) return fail(W4A_ERR_SHAPE, "window %d", window);
+  if (table_width < 1 || (long long)table_width * page_size >= (1LL << 30))
+    return fail(W4A_ERR_SHAPE, "table_width %d (fewer than 2^30 positions)", table_width);
+  if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(ws))
+    return fail(W4A_ERR_ALIGN, "misaligned pointer");
+  const size_t qb = (size_t)rows * n_heads * head_dim * 2;
+  if (overlap(q, qb, out, qb)) return fail(W4A_ERR_ARG, "out overlaps q");
+  DevInfo* di;
+  rc = device_info(&di);
+  if (rc) return rc;
+  const size_t need = attn_shared_ws(rows, batch, n_heads, n_kv_heads, head_dim, max_new, di->sms);
+  if (ws_bytes < need) return fail(W4A_ERR_WORKSPACE, "workspace %zu < %zu bytes", ws_bytes, need);
+  CK(launch_attn_shared(q, rows, batch, n_heads, n_kv_heads, head_dim, k_pages, v_pages, n_pages, page_size, row_start,
+                        lens, table, table_width, prefix_table, prefix_len, window, max_new, out,
+                        static_cast<uint8_t*>(ws), di->sms, S(stream)));
+  return W4A_OK;
+}
+
 int w4a_trace(void* buf, size_t bytes) {
   if (buf && !aligned16(buf)) return fail(W4A_ERR_ALIGN, "trace buffer not 16-byte aligned");
   g_trace = buf;
@@ -1169,6 +1343,8 @@ int w4a_check(const void* ws, size_t ws_bytes, void* stream) {
     return fail(W4A_ERR_TIMEOUT, "device wait timed out (error word 0x%x)", e);
   if (e & EW_RANGE)
     return fail(W4A_ERR_KERNEL, "an fp16 intermediate (SwiGLU or attention output) overflowed (error word 0x%x)", e);
+  if (e & EW_PAGES)
+    return fail(W4A_ERR_KERNEL, "a paged plan ran out of pages, table width or rows (error word 0x%x)", e);
   if (e) return fail(W4A_ERR_KERNEL, "device error word 0x%x", e);
   return W4A_OK;
 }

@@ -454,15 +454,6 @@ struct FaArgs {
   uint32_t* err;
 };
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 template <int HD>
 __global__ void __launch_bounds__(FA_THREADS, 3) flash_prefill_kernel(const FaArgs a) {
   constexpr int CH = HD / 8;            // 16-byte chunks per row

@@ -37,6 +37,8 @@ constexpr int XSUM_BYTES = 6912;       // per-128-group sums of x: [groups][8 * 
 __host__ __device__ constexpr int wsp_bytes(int nb) { return NW * 2 * 32 * 4 * nb * 4; }
 constexpr int MAX_B = 16;
 constexpr int MAX_LAYERS = 128;
+constexpr int MAX_PAGED_BATCH = 4096;  // sequences of one call on the paged cache
+constexpr int MAX_PAGED_GQ = 16;       // query heads per KV head on the paged cache
 constexpr int MAX_GQ = 8;              // query heads per KV head supported by the attention tile
 // A GEMV phase whose K is split into more than RED_NS slabs (batch > 1) sums
 // them itself: the last CTA to finish a row block adds the slabs in order, so
@@ -56,6 +58,7 @@ enum : uint32_t {
   EW_BAD_SHAPE = 1u << 3,        // device-side shape check failed
   EW_BAD_POS = 1u << 4,          // a position outside the cache
   EW_RANGE = 1u << 5,            // a value carried in fp16 (SwiGLU or attention output) overflowed
+  EW_PAGES = 1u << 6,            // a paged plan ran out of free pages, table width or rows
 };
 
 // ---- engine modes / phase kinds --------------------------------------------

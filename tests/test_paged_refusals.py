@@ -71,7 +71,7 @@ def attn_args(**kw):
     (dict(q=None), "ARG"), (dict(lens=None), "ARG"), (dict(ptab=None), "ARG"), (dict(rows=0), "SHAPE"),
     (dict(rows=(1 << 20) + 1), "SHAPE"), (dict(batch=0), "SHAPE"), (dict(nq=34), "SHAPE"), (dict(hd=32), "UNSUPPORTED"),
     (dict(page=24), "SHAPE"), (dict(P_=-1), "SHAPE"), (dict(window=-1), "SHAPE"), (dict(max_new=0), "SHAPE"),
-    (dict(width=0), "SHAPE"), (dict(width=1 << 26), "SHAPE"), (dict(k=P(0x1008)), "ALIGN"), (dict(out=P(0x100000)), "ARG")])
+    (dict(width=0), "SHAPE"), (dict(width=1 << 26), "SHAPE"), (dict(width=1 << 25, batch=128), "SHAPE"), (dict(k=P(0x1008)), "ALIGN"), (dict(out=P(0x100000)), "ARG")])
 def test_attn_refusals(lib, kw, code):
     assert lib.w4a_attn_shared(*attn_args(**kw)) == getattr(_abi, "ERR_" + code)
 

@@ -730,19 +730,6 @@ __device__ __forceinline__ void ft_gather(uint8_t* dst, const uint16_t* cache, c
   cp_async_commit();
 }
 
-// 2^x on the special-function unit (results below 2^-126 flush to zero)
-__device__ __forceinline__ float ex2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-// Two floats rounded to bf16 in one conversion (lo in the low half).
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
 __global__ void __launch_bounds__(FT_THREADS, 1)
     flash_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKc,

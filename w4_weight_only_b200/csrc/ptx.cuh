@@ -122,6 +122,26 @@ __device__ __forceinline__ uint64_t globaltimer() {
   return t;
 }
 
+// ---- dependent launches ------------------------------------------------------------
+// Lets the next kernel of the stream start (when it was launched with the
+// programmatic attribute) once every CTA has got here or left.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Waits until the kernel before this one has finished and its writes are seen.
+__device__ __forceinline__ void wait_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// 2^x on the special-function unit (results below 2^-126 flush to zero)
+__device__ __forceinline__ float ex2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two floats rounded to bf16 in one conversion (lo in the low half).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
 // ---- tensor cores ---------------------------------------------------------------
 // D = A(16x16, row) * B(16x8, col) + C, bf16 inputs, fp32 accumulate.
 __device__ __forceinline__ void mma_16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,

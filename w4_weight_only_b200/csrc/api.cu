@@ -1141,7 +1141,7 @@ static int check_pages(int n_pages, int page_size, int n_kv_heads) {
 // packs at most MAX_GQ query heads per KV head.
 static int check_paged_heads(int nq, int nkv, int hd) {
   if (hd != 64 && hd != 128) return fail(W4A_ERR_UNSUPPORTED, "head_dim %d", hd);
-  if (nkv < 1 || nq < 1 || nq % nkv || nq / nkv > MAX_PAGED_GQ || nq > 1024)
+  if (nkv < 1 || nkv > MAX_PAGED_KV || nq < 1 || nq % nkv || nq / nkv > MAX_PAGED_GQ)
     return fail(W4A_ERR_SHAPE, "heads %d / kv heads %d", nq, nkv);
   return W4A_OK;
 }

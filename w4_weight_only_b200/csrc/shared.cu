@@ -36,7 +36,7 @@ namespace w4a {
 namespace {
 
 constexpr long long SH_WAIT = 4000000000LL;  // bound on any single wait (~2 s)
-constexpr int FEW = 16;                      // packed rows of a sequence that few_kernel takes
+constexpr int MAX_FEW = 48;                  // packed rows of a sequence that few_kernel takes, at most
 constexpr float RESCALE = 8.f;               // the kept reference may fall this far (log2) below the maximum
 
 struct ShArgs {
@@ -49,13 +49,14 @@ struct ShArgs {
   uint32_t* err;
   float* o_part;        // [parts][rows * nq][HD]
   float2* ml_part;      // [parts][rows * nq]: (m, l)
-  float* o_cont;        // [G][FEW][HD]: pieces that begin inside a segment
-  float2* ml_cont;      // [G][FEW]
-  int32_t* cum;         // [batch + 2]: few_kernel's key tiles before each sequence
+  float* o_cont;        // [G][few][HD]: pieces that begin inside a segment
+  float2* ml_cont;      // [G][few]
   int rows, batch, nq, nkv, gq, n_pages, page_log2, width, P, window, max_new;
   int ns_prefix;        // pieces of the prefix (slots 0 ..), 0 without one
   int ns_own;           // pieces of the own positions in tc_kernel (slots ns_prefix ..)
+  int few;              // packed rows of a sequence that few_kernel takes (16, 32 or 48)
   int prefix_few;       // 1: few_kernel takes the prefix too (few packed rows in all)
+  int own_joins;        // 1: tc_kernel's own pieces (one each) take in the prefix's and write the output
   int G;                // CTAs of few_kernel
   float scale_log2;     // log2(e) / sqrt(hd)
 };
@@ -110,7 +111,7 @@ __device__ __forceinline__ void sh_drain(uint64_t* bar, uint32_t par, uint32_t* 
 // page (or part of one) and panel.  Pages at or past key_end are not in the
 // list; their rows of the tile keep what was there.
 // ---------------------------------------------------------------------------
-template <int HD, int ROWS>
+template <int ROWS>
 __device__ __forceinline__ uint32_t load_blocks(int kb, int key_end, int page_log2) {
   const int bs = min(1 << page_log2, ROWS);
   return uint32_t((min(ROWS, key_end - kb) + bs - 1) / bs);  // blocks of bs keys to copy
@@ -120,7 +121,7 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
                                           int key_end, int kvh, uint64_t* bar, const ShArgs& a, int lane) {
   constexpr int PANELS = HD / 64;
   const int bs = min(1 << a.page_log2, ROWS);
-  const int nblk = int(load_blocks<HD, ROWS>(kb, key_end, a.page_log2));
+  const int nblk = int(load_blocks<ROWS>(kb, key_end, a.page_log2));
   if (lane < nblk * PANELS) {
     const int blk = lane / PANELS, panel = lane % PANELS;
     const int k0 = kb + blk * bs;
@@ -145,33 +146,38 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
 //  PAIR: two tiles of 128 rows, group i has tile i, both use every K / V tile.
 //  ALT (at most 128 rows): one tile of rows, group i has the key tiles of
 //        parity i, and the groups' pieces are joined at the end.
-// S_i = Q K^T into TMEM columns [128 i, + 128); the group reads its rows,
-// forms P = 2^(s - m) and writes it back as bf16 pairs over the first 64 of
-// the same columns (head_dim 64: next to O), where the second MMA reads it as
-// its A operand: O_i += P V, V as an MN-major operand.  The reference m moves
-// only when the maximum has risen by more than 2^8 over it, so O is rescaled
-// rarely; P <= 2^8 is rounded to bf16, 2^-8 of each weight at most, while l
-// sums the weights unrounded in fp32.
+// S_i = Q K^T into TMEM columns [128 i, + 128); the group reads its rows twice
+// (32 columns at a time: the maximum, then the weights; a second read of TMEM
+// costs less than 128 registers and four times the code), forms P = 2^(s - m)
+// and writes it back as bf16 pairs over the first 64 of the same columns
+// (head_dim 64: next to O), where the second MMA reads it as its A operand,
+// O_i += P V, V as an MN-major operand; it starts on the first 64 keys while
+// the weights of the others are formed.  The reference m moves only when the
+// maximum has risen by more than 2^8 over it, so O is rescaled rarely; P <=
+// 2^8 is rounded to bf16, 2^-8 of each weight at most, while l sums the
+// weights unrounded in fp32.
 template <int HD, bool ALT>
 struct Tc {
   static constexpr int TILE = 128 * HD * 2;                 // 128 rows, bytes
   static constexpr int PANEL = 128 * 128;
   static constexpr int NQ = ALT ? 1 : 2;
-  static constexpr int NS = HD == 128 ? (ALT ? 5 : 4) : 8;  // K / V ring slots
+  static constexpr int NS = HD == 128 ? (ALT ? 3 : 4) : (ALT ? 6 : 8);  // K / V ring slots
   static constexpr int ROWS = NQ * 128;
-  static constexpr int BARS = 256;
+  static constexpr int BARS = 512;
   static constexpr int SMEM = (NQ + NS) * TILE + BARS + 1024;
   static constexpr int O_COL = 256;                         // O_i at 256 + i HD
   static constexpr int P_COL(int i) { return HD == 128 ? i * 128 : 384 + i * 64; }
+  static constexpr int LD = HD + 4;                         // floats between the rows of O in shared memory
+  static_assert(NQ * 128 * (LD * 4 + 16) <= (NQ + NS) * TILE, "O tiles fit where Q, K and V were");
 };
 constexpr int TC_THREADS = 320;
 
 template <int HD, bool ALT>
-__global__ void __launch_bounds__(TC_THREADS, 1)
+__global__ void __launch_bounds__(TC_THREADS, 1) __maxnreg__(ALT ? 128 : 168)
     tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-              const __grid_constant__ ShArgs a, const int own) {
+              const __grid_constant__ ShArgs a, const int own, const int lead) {
   using C = Tc<HD, ALT>;
-  constexpr int NS = C::NS, TILE = C::TILE, PANEL = C::PANEL;
+  constexpr int NS = C::NS, TILE = C::TILE, PANEL = C::PANEL, LD = C::LD;
   extern __shared__ uint8_t tc_raw[];
   uint8_t* sm = tc_raw + ((1024u - (smem_addr(tc_raw) & 1023u)) & 1023u);
   uint8_t* sQ = sm;
@@ -180,16 +186,38 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   uint64_t* kv_full = q_full + 1;        // [NS]
   uint64_t* kv_empty = kv_full + NS;     // [NS]
   uint64_t* s_full = kv_empty + NS;      // [2]: S_i computed (and every earlier MMA done)
-  uint64_t* p_full = s_full + 2;         // [2]: P_i written, O_i rescaled (4 warps arrive)
-  uint64_t* o_done = p_full + 2;
+  uint64_t* p_full = s_full + 2;         // [2][2]: half of P_i written, O_i rescaled (4 warps arrive)
+  uint64_t* o_done = p_full + 4;
   uint32_t* tbase = reinterpret_cast<uint32_t*>(o_done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tbase + 1);
   int* s_lo = reinterpret_cast<int*>(tbase + 2);
-  int* s_hi = s_lo + 1;
-  int* s_b = s_hi + 1;      // sequence and its first tile
+  int* s_b = s_lo + 1;      // sequence and its first tile
   int* s_warp = s_b + 2;    // [8]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    mbar_init(q_full, 8);
+#pragma unroll 1
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(kv_full + s, 1);
+      mbar_init(kv_empty + s, 1);
+    }
+#pragma unroll 1
+    for (int s = 0; s < 2; ++s) mbar_init(s_full + s, 1);
+#pragma unroll 1
+    for (int s = 0; s < 4; ++s) mbar_init(p_full + s, 4);
+    mbar_init(o_done, 1);
+    *abort_flag = 0;
+    *s_lo = a.P;
+    s_b[0] = -1;
+    fence_mbar_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(tbase, 512);
+    tmem_relinquish();
+  }
+
+  if (lead) wait_previous_kernel();  // first launch of the call: nothing is read before what came before it is done
   launch_dependents();
 
   // ---- which item: KV head, rows [base, base + valid) of the packed rows of
@@ -213,14 +241,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     x /= ns;
     kvh = x % a.nkv;
     const int want = x / a.nkv;  // tile of the sequences with many rows, in order
-    if (tid == 0) s_b[0] = -1;
     int before = 0;
 #pragma unroll 1
     for (int c0 = 0; c0 < a.batch; c0 += 256) {
       int t = 0;
       if (tid < 256 && c0 + tid < a.batch) {
         const Seq s = load_seq(a, c0 + tid);
-        if (s.n * a.gq > FEW) t = (s.n * a.gq + C::ROWS - 1) / C::ROWS;
+        if (s.n * a.gq > a.few) t = (s.n * a.gq + C::ROWS - 1) / C::ROWS;
       }
       int incl = t;
 #pragma unroll
@@ -258,81 +285,64 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       valid = min(C::ROWS, n * a.gq - base);
     }
   }
-  if (valid <= 0) {  // uniform: nothing here
-    wait_previous_kernel();
-    return;
-  }
 
-  if (tid == 0) {
-    mbar_init(q_full, 8);
-#pragma unroll 1
-    for (int s = 0; s < NS; ++s) {
-      mbar_init(kv_full + s, 1);
-      mbar_init(kv_empty + s, 1);
-    }
-    mbar_init(s_full + 0, 1);
-    mbar_init(s_full + 1, 1);
-    mbar_init(p_full + 0, 4);
-    mbar_init(p_full + 1, 4);
-    mbar_init(o_done, 1);
-    *abort_flag = 0;
-    *s_lo = 0x7fffffff;
-    *s_hi = 0;
-    fence_mbar_init();
-    tma_prefetch_map(&tmK);
-    tma_prefetch_map(&tmV);
-  }
-  if (warp == 9) {
-    tmem_alloc(tbase, 512);
-    tmem_relinquish();
-  }
-  __syncthreads();
-  // ---- this thread's row: token, head, visible keys [vlo, vhi) (prefix
-  // positions, or own positions) ----
+  // ---- this thread's row: token, head, its query; the visible keys [vlo,
+  // vhi) (prefix positions, or own positions) ----
   const int grp = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
   const int prow = base + (ALT ? 0 : grp * 128) + r;
   const bool live = warp < 8 && prow < base + valid;
-  const int tok = live ? r0 + prow / a.gq : 0, head = kvh * a.gq + (live ? prow % a.gq : 0);
-  int vlo = 0, vhi = 0;
+  const int row_tok = live ? prow / a.gq : 0;
+  const int tok = r0 + row_tok, head = kvh * a.gq + (live ? prow - row_tok * a.gq : 0);
+  constexpr int CH = HD / 8, QN = ALT ? CH / 2 : CH;  // 16-byte chunks of a row; of it that this thread brings
+  const int qc0 = ALT ? grp * QN : 0;
+  uint4 qv[QN];
   if (live) {
-    if (own) {
-      const int p = len - n + prow / a.gq;  // own position of the row
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)tok * a.nq + head) * HD) + qc0;
+#pragma unroll
+    for (int c = 0; c < QN; ++c) qv[c] = src[c];
+  }
+  int vlo = 0, vhi = 0, k_lo = 0, k_hi = a.P;  // k: keys that some row of the item sees
+  if (own) {
+    k_hi = len - n + (base + valid - 1) / a.gq + 1;
+    if (a.window) k_lo = max(0, len - n + base / a.gq - a.window + 1);
+    if (live) {
+      const int p = len - n + row_tok;  // own position of the row
       vhi = p + 1;
       if (a.window) vlo = max(0, p - a.window + 1);
-    } else {
-      vhi = a.P;
-      if (a.window) {
-        // the row's sequence: the last one that starts at or before it
-        int lo = 0, hi = a.batch;
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (a.row_start[mid] <= tok)
-            lo = mid;
-          else
-            hi = mid;
-        }
-        const Seq s = load_seq(a, lo);
-        const int back = s.len - s.n + (tok - s.r0);  // own positions before the row's
-        vlo = s.n ? min(a.P, max(0, a.P + back - a.window + 1)) : a.P;
-      }
     }
-    if (vlo < vhi) {
-      atomicMin(s_lo, vlo);
-      atomicMax(s_hi, vhi);
+  } else if (live) {
+    vhi = a.P;
+    if (a.window) {
+      // the row's sequence: the last one that starts at or before it
+      int lo = 0, hi = a.batch;
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.row_start[mid] <= tok)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      const Seq s = load_seq(a, lo);
+      const int back = s.len - s.n + (tok - s.r0);  // own positions before the row's
+      vlo = s.n ? min(a.P, max(0, a.P + back - a.window + 1)) : a.P;
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (!own && a.window) {  // uniform
+    if (live) atomicMin(s_lo, vlo);
+    __syncthreads();
+    k_lo = *s_lo;
+  }
   const uint32_t tmem = *tbase;
-  const int k_lo = *s_lo, k_hi = *s_hi;  // keys that some row of the item sees
   int t0 = 0, nb = 0;
-  if (k_lo < k_hi) {
+  if (k_lo < k_hi && valid > 0) {
     const int f = k_lo >> 7, nt = ((k_hi + 127) >> 7) - f;
     t0 = f + int((long long)nt * piece / ns);
     nb = f + int((long long)nt * (piece + 1) / ns) - t0;
   }
-  const int groups = (ALT ? nb > 1 : valid > 128) ? 2 : 1;
+  const int groups = valid <= 0 ? 0 : ((ALT ? nb > 1 : valid > 128) ? 2 : 1);
   const int32_t* pages = own ? a.table + (size_t)b * a.width : a.ptable;
 
   if (warp == 8) {
@@ -352,7 +362,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       const int kb = (t0 + t) * 128;
       const int bs = min(1 << a.page_log2, 128);
-      if (lane == 0) mbar_expect_tx(kv_full + s, load_blocks<HD, 128>(kb, k_hi, a.page_log2) * bs * HD * 2);
+      if (lane == 0) mbar_expect_tx(kv_full + s, load_blocks<128>(kb, k_hi, a.page_log2) * bs * HD * 2);
       __syncwarp();
       load_tile<HD, 128>(sR + s * TILE, map, pages, kb, k_hi, kvh, kv_full + s, a, lane);
       ++it;
@@ -397,17 +407,21 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
         umma_commit(s_full + qi);
       };
-      auto issue_pv = [&](int qi, uint32_t vi, bool first) {
+      // O_qi (+)= P_qi V: each half of the keys when its weights are there
+      auto issue_pv = [&](int qi, uint32_t vi, int j) {
         const uint8_t* v = sR + (vi % NS) * TILE;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          umma_f16_ts(tmem + uint32_t(C::O_COL + qi * HD), tmem + uint32_t(C::P_COL(qi) + ks * 8),
-                      umma_desc_mn_sw128(v + ks * 16 * 128, PANEL, 1024), idO, (first && ks == 0) ? 0u : 1u);
-      };
-      auto p_ready = [&](int qi, int j) {
-        const bool w = sh_wait(p_full + qi, uint32_t(j) & 1u, abort_flag, a.err);
-        tc_fence_after();
-        return w;
+        for (int half = 0; half < 2; ++half) {
+          if (!sh_wait(p_full + qi * 2 + half, uint32_t(j) & 1u, abort_flag, a.err)) return false;
+          tc_fence_after();
+#pragma unroll
+          for (int k4 = 0; k4 < 4; ++k4) {
+            const int ks = half * 4 + k4;
+            umma_f16_ts(tmem + uint32_t(C::O_COL + qi * HD), tmem + uint32_t(C::P_COL(qi) + ks * 8),
+                        umma_desc_mn_sw128(v + ks * 16 * 128, PANEL, 1024), idO, (j == 0 && ks == 0) ? 0u : 1u);
+          }
+        }
+        return true;
       };
       bool ok = sh_wait(q_full, 0u, abort_flag, a.err);
       uint32_t it = 0;
@@ -421,8 +435,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         }
 #pragma unroll 1
         for (int t = 0; t < nb && ok; ++t) {
-          if (!(ok = ready(it) && p_ready(t & 1, t >> 1))) break;
-          issue_pv(t & 1, it, t < 2);
+          if (!(ok = ready(it) && issue_pv(t & 1, it, t >> 1))) break;
           umma_commit(kv_empty + it % NS);
           ++it;
           if (t + 2 < nb) {
@@ -442,15 +455,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         for (int j = 0; j < nb && ok; ++j) {
           const uint32_t vt = 2u * j + 1u, kn = 2u * j + 2u;
           const bool more = j + 1 < nb;
-          if (!(ok = ready(vt) && p_ready(0, j))) break;
-          issue_pv(0, vt, j == 0);
+          if (!(ok = ready(vt) && issue_pv(0, vt, j))) break;
           if (more) {
             if (!(ok = ready(kn))) break;
             issue_s(0, kn);
           }
           if (groups == 2) {
-            if (!(ok = p_ready(1, j))) break;
-            issue_pv(1, vt, j == 0);
+            if (!(ok = issue_pv(1, vt, j))) break;
             umma_commit(kv_empty + vt % NS);
             if (more) issue_s(1, kn);
           } else {
@@ -465,20 +476,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     }
   } else {
     // ---- the rows of Q into shared memory (128-byte swizzle; ALT: half of each row per group) ----
-    {
-      const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)tok * a.nq + head) * HD);
-      constexpr int CH = HD / 8;
-      const int c0 = ALT ? grp * (CH / 2) : 0, c1 = ALT ? c0 + CH / 2 : CH;
+    if (live) {
       uint8_t* dst = sQ + (ALT ? 0 : grp) * TILE + r * 128;
-      if (live) {
-#pragma unroll 8
-        for (int c = c0; c < c1; ++c)
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * PANEL + (((c & 7) ^ (r & 7)) << 4)) = src[c];
+#pragma unroll
+      for (int k = 0; k < QN; ++k) {
+        const int c = qc0 + k;
+        *reinterpret_cast<uint4*>(dst + (c >> 3) * PANEL + (((c & 7) ^ (r & 7)) << 4)) = qv[k];
       }
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
     }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(q_full);
     // ---- softmax ----
     const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t tS = tl + uint32_t(grp * 128), tP = tl + uint32_t(C::P_COL(grp)),
@@ -486,11 +494,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     const bool warp_live = __any_sync(0xffffffffu, live);
     float m_run = -INFINITY, l_run = 0.f;
     bool ok = true;
-    const int step = ALT ? 2 : 1;
     int j = 0;
     if (grp < groups) {
 #pragma unroll 1
-      for (int t = ALT ? grp : 0; t < nb; t += step, ++j) {
+      for (int t = ALT ? grp : 0; t < nb; t += ALT ? 2 : 1, ++j) {
         const int kb = (t0 + t) * 128;
         // keys that no row sees: their values must be finite (0 x NaN), so
         // group 0 (ALT: the tile's group) clears those rows of V
@@ -514,128 +521,197 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           fence_proxy_async();
         }
+        const int ilo = vlo - kb, ihi = vhi - kb;  // visible: ilo <= i < ihi
+        const bool part = __any_sync(0xffffffffu, live && (ilo > 0 || ihi < 128));
+        auto hide = [&](uint32_t (&v)[32], int c0) {
+          if (part) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (c0 + i < ilo || c0 + i >= ihi) v[i] = 0xff800000u;  // -inf
+          }
+        };
+        uint32_t v0[32], v1[32];
+        float mx = -INFINITY;
         if (warp_live) {
-          uint32_t v[128];
+          auto top = [&](uint32_t (&v)[32], int c0) {
+            hide(v, c0);
+            float m0 = mx, m1 = __uint_as_float(v[1]);
 #pragma unroll
-          for (int c = 0; c < 128; c += 32) tmem_ld32(tS + uint32_t(c), v + c);
-          tmem_ld_wait();
-          const int ilo = vlo - kb, ihi = vhi - kb;  // visible: ilo <= i < ihi
-          if (ilo > 0 || ihi < 128) {
+            for (int i = 0; i < 32; i += 4) {
+              m0 = fmaxf(fmaxf(m0, __uint_as_float(v[i])), __uint_as_float(v[i + 2]));
+              m1 = fmaxf(fmaxf(m1, __uint_as_float(v[i + 1])), __uint_as_float(v[i + 3]));
+            }
+            mx = fmaxf(m0, m1);
+          };
+          tmem_ld32(tS, v0);
 #pragma unroll
-            for (int i = 0; i < 128; ++i)
-              if (i < ilo || i >= ihi) v[i] = 0xff800000u;  // -inf
+          for (int c = 0; c < 128; c += 64) {
+            tmem_ld_wait32(v0);
+            tmem_ld32(tS + uint32_t(c + 32), v1);
+            top(v0, c);
+            tmem_ld_wait32(v1);
+            tmem_ld32(tS + uint32_t(c == 0 ? 64 : 0), v0);  // last: the first columns again, for the weights
+            top(v1, c + 32);
           }
-          float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 128; i += 4) {
-            mx0 = fmaxf(mx0, __uint_as_float(v[i]));
-            mx1 = fmaxf(mx1, __uint_as_float(v[i + 1]));
-            mx2 = fmaxf(mx2, __uint_as_float(v[i + 2]));
-            mx3 = fmaxf(mx3, __uint_as_float(v[i + 3]));
-          }
-          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * a.scale_log2;
+          mx *= a.scale_log2;
           float alpha = 1.f;
           if (mx > m_run + RESCALE) {  // also the first finite maximum of the row
             alpha = exp2f(m_run - mx);  // 0 while the reference was -inf
             m_run = mx;
           }
-          const float nref = m_run == -INFINITY ? 0.f : -m_run;
-          float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-          for (int i = 0; i < 128; i += 2) {
-            const float p0 = ex2_fast(fmaf(__uint_as_float(v[i]), a.scale_log2, nref));
-            const float p1 = ex2_fast(fmaf(__uint_as_float(v[i + 1]), a.scale_log2, nref));
-            sum0 += p0;
-            sum1 += p1;
-            v[i >> 1] = cvt_bf16x2(p0, p1);
-          }
-          tmem_st32(tP, v);
-          tmem_st32(tP + 32u, v + 32);
-          l_run = l_run * alpha + (sum0 + sum1);
+          l_run *= alpha;
           // O rows whose reference moved (the group's previous P V has completed: S_i's barrier follows it)
           if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            tmem_ld_wait32(v0);
 #pragma unroll 1
             for (int c = 0; c < HD; c += 32) {
-              uint32_t o[32];
-              tmem_ld32(tO + uint32_t(c), o);
-              tmem_ld_wait();
+              tmem_ld32(tO + uint32_t(c), v1);
+              tmem_ld_wait32(v1);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tmem_st32(tO + uint32_t(c), o);
+              for (int i = 0; i < 32; ++i) v1[i] = __float_as_uint(__uint_as_float(v1[i]) * alpha);
+              tmem_st32(tO + uint32_t(c), v1);
             }
           }
-          tmem_st_wait();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(p_full + grp);
+        const float nref = m_run == -INFINITY ? 0.f : -m_run;
+        const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), nref2 = pack_f32x2(nref, nref);
+        uint64_t sum2 = 0;
+        auto weights = [&](uint32_t (&v)[32], int c0) {
+          hide(v, c0);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint64_t x =
+                fma_f32x2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale2, nref2);
+            float x0, x1;
+            unpack_f32x2(x, x0, x1);
+            const float p0 = ex2_fast(x0), p1 = ex2_fast(x1);
+            sum2 = add_f32x2(sum2, pack_f32x2(p0, p1));
+            v[i >> 1] = cvt_bf16x2(p0, p1);
+          }
+          tmem_st16(tP + uint32_t(c0 >> 1), v);
+        };
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          if (warp_live) {
+            tmem_ld_wait32(v0);
+            tmem_ld32(tS + uint32_t(half * 64 + 32), v1);
+            weights(v0, half * 64);
+            tmem_ld_wait32(v1);
+            if (half == 0) tmem_ld32(tS + 64u, v0);
+            weights(v1, half * 64 + 32);
+            tmem_st_wait();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + grp * 2 + half);
+        }
+        float s0, s1;
+        unpack_f32x2(sum2, s0, s1);
+        l_run += s0 + s1;
       }
     }
-    // ---- outputs ----
+    // ---- outputs: the rows of O through shared memory, so that they are
+    // written whole; (m, l) of each row beside them ----
     ok = ok && (nb == 0 || __all_sync(0xffffffffu, sh_wait(o_done, 0u, abort_flag, a.err)));
     tc_fence_after();
-    float* xO = reinterpret_cast<float*>(sR);         // ALT: group 1's piece, [HD][128] then (m, l) [128]
-    float2* xml = reinterpret_cast<float2*>(xO + HD * 128);
     const bool join = ALT && groups == 2;
-    if (join) {
-      if (grp == 1 && ok && warp_live) {
+    float* sO = reinterpret_cast<float*>(sm) + (ALT ? 0 : grp * 128 * LD);  // [128][LD]
+    float4* s_row = reinterpret_cast<float4*>(sm + C::NQ * 128 * LD * 4) + (ALT ? 0 : grp * 128);
+    float* mine = sO + r * LD;
+    auto dump = [&](float f, bool add, float g) {
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(tO + uint32_t(c), o);
-          tmem_ld_wait();
+      for (int c = 0; c < HD; c += 32) {
+        uint32_t o[32];
+        tmem_ld32(tO + uint32_t(c), o);
+        tmem_ld_wait();
 #pragma unroll
-          for (int i = 0; i < 32; ++i) xO[(c + i) * 128 + r] = __uint_as_float(o[i]);
+        for (int i = 0; i < 32; i += 4) {
+          float4 x = make_float4(__uint_as_float(o[i]) * f, __uint_as_float(o[i + 1]) * f,
+                                 __uint_as_float(o[i + 2]) * f, __uint_as_float(o[i + 3]) * f);
+          float4* d = reinterpret_cast<float4*>(mine + c + i);
+          if (add) {
+            const float4 y = *d;
+            x = make_float4(fmaf(y.x, g, x.x), fmaf(y.y, g, x.y), fmaf(y.z, g, x.z), fmaf(y.w, g, x.w));
+          }
+          *d = x;
         }
-        xml[r] = make_float2(m_run, l_run);
+      }
+    };
+    if (join) {
+      if (grp == 1 && warp_live && ok) {
+        dump(1.f, false, 0.f);
+        s_row[r] = make_float4(m_run, l_run, 0.f, 0.f);
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
-    if (grp < (ALT ? 1 : groups) && ok && warp_live) {
-      const bool direct = own && a.ns_prefix == 0 && a.ns_own == 1;
+    if (grp < (ALT ? min(groups, 1) : groups) && warp_live && ok) {
       float f0 = 1.f, f1 = 0.f;
       if (join) {
-        const float2 o = xml[r];
+        const float4 o = s_row[r];
         const float M = fmaxf(m_run, o.x);
         f0 = m_run == -INFINITY ? 0.f : exp2f(m_run - M);
         f1 = o.x == -INFINITY ? 0.f : exp2f(o.x - M);
         m_run = M;
         l_run = l_run * f0 + o.y * f1;
       }
-      if (direct) {
-        const float inv = l_run > 0.f ? 1.f / l_run : 0.f;
-        f0 *= inv;
-        f1 *= inv;
-      }
-      const int part = own ? a.ns_prefix + piece : piece;
-      const size_t prow_at = ((size_t)part * a.rows + tok) * a.nq + head;
-      if (!direct && live) a.ml_part[prow_at] = make_float2(m_run, l_run);
-      if (nb > 0) {
+      const bool final = own && a.own_joins;
+      const size_t stride = (size_t)a.rows * a.nq;
+      const int np = final ? a.ns_prefix : 0;
+      if (np > 0) wait_previous_kernel();  // the prefix's pieces, made by the launch before this one
+      if (final) {
+        // the weights of this piece and of the prefix's in the joined row
+        const size_t line = (size_t)tok * a.nq + head;
+        const float m0 = m_run;
+        float L = l_run;
+        if (live) {
 #pragma unroll 1
-        for (int c = 0; c < HD; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(tO + uint32_t(c), o);
-          tmem_ld_wait();
-          float x[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            x[i] = __uint_as_float(o[i]) * f0;
-            if (join) x[i] = fmaf(xO[(c + i) * 128 + r], f1, x[i]);
+          for (int i = 0; i < np; ++i) {
+            const float2 ml = a.ml_part[i * stride + line];
+            if (!(ml.y > 0.f)) continue;
+            const float M = fmaxf(m_run, ml.x);
+            L = L * exp2f(m_run - M) + ml.y * exp2f(ml.x - M);
+            m_run = M;
           }
-          if (live) {
-            if (direct) {
-              uint16_t* dst = a.out + ((size_t)tok * a.nq + head) * HD + c;
-#pragma unroll
-              for (int i = 0; i < 32; i += 8)
-                *reinterpret_cast<uint4*>(dst + i) =
-                    make_uint4(cvt_bf16x2(x[i], x[i + 1]), cvt_bf16x2(x[i + 2], x[i + 3]),
-                               cvt_bf16x2(x[i + 4], x[i + 5]), cvt_bf16x2(x[i + 6], x[i + 7]));
-            } else {
-              float* dst = a.o_part + prow_at * HD + c;
-#pragma unroll
-              for (int i = 0; i < 32; i += 4)
-                *reinterpret_cast<float4*>(dst + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-            }
+        }
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const float f = live ? exp2f(m0 - m_run) * inv : 0.f;
+        f0 *= f;
+        f1 *= f;
+        l_run = inv;
+      }
+      if (nb > 0) dump(f0, join, f1);
+      // (m, l), or with the final row (reference, 1 / sum); which row of the outputs
+      s_row[r] = make_float4(m_run, l_run, __int_as_float(tok * a.nq + head), 0.f);
+      __syncwarp();
+      // a warp writes its 32 rows, one after the other, 16 bytes a lane
+      const int w0 = (warp & 3) * 32, rows = min(32, valid - (ALT ? 0 : grp * 128) - w0);
+      const int part = own ? a.ns_prefix + piece : piece;
+      constexpr int LPR = HD / 4;  // lanes of a row
+      const int sub = lane / LPR, col = (lane % LPR) * 4;
+      if (final) {
+#pragma unroll 4
+        for (int i = sub; i < rows; i += 32 / LPR) {
+          float4 x = *reinterpret_cast<const float4*>(sO + (w0 + i) * LD + col);
+          const float4 w = s_row[w0 + i];
+          const size_t line = size_t(__float_as_int(w.z));
+          for (int k = 0; k < np; ++k) {
+            const float2 ml = a.ml_part[k * stride + line];
+            if (!(ml.y > 0.f)) continue;
+            const float f = exp2f(ml.x - w.x) * w.y;
+            const float4 y = *reinterpret_cast<const float4*>(a.o_part + (k * stride + line) * HD + col);
+            x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+          }
+          *reinterpret_cast<uint2*>(a.out + line * HD + col) = make_uint2(cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w));
+        }
+      } else {
+        float* o_part = a.o_part + part * stride * HD + col;
+        if (live) a.ml_part[part * stride + tok * a.nq + head] = make_float2(m_run, l_run);
+        if (nb > 0) {
+#pragma unroll 8
+          for (int i = sub; i < rows; i += 32 / LPR) {
+            const float4 x = *reinterpret_cast<const float4*>(sO + (w0 + i) * LD + col);
+            const int line = __float_as_int(s_row[w0 + i].z);
+            *reinterpret_cast<float4*>(o_part + (size_t)line * HD) = x;
           }
         }
       }
@@ -653,86 +729,124 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 // ---------------------------------------------------------------------------
 // few_kernel
 // ---------------------------------------------------------------------------
-// The 64-key tiles of every (sequence, KV head) with at most 16 packed rows
-// form one stream (sequence, then KV head, then key), cut into G equal runs,
-// one a CTA, whatever the lengths: a CTA takes the segments of its run one by
-// one.  A segment that lies in one run is finished there; the piece with its
-// first tile goes to the rows' own slot, a piece that begins inside a segment
-// to the CTA's (a run has one such piece at most, its first).
-// Warps 0-3 compute, warp 4 loads (a ring of stages of 64 K rows and 64 V
-// rows, running ahead over segments).  Per tile warp w forms the scores of
-// keys 16 w .. + 15 with mma.sync (16 rows by 16 keys), the warps exchange
-// their rows' maxima, write P to shared memory, and each multiplies the whole
-// P with its quarter of V's columns; so O is never summed across warps.
-// mma.sync, since 16 rows would fill an eighth of a tcgen05 tile and memory
-// bounds this kernel.  The tensor pipe is idle most of the time, so P goes in
-// as two bf16 terms, P and its rounding error, for two products.
-template <int HD>
+// The 64-key tiles of every (sequence, KV head) with at most 16 MG packed rows
+// form one stream (sequence, then KV head, then key), cut into G equal
+// runs, one a CTA, whatever the lengths: a CTA takes the segments of its run
+// one by one.  A segment that lies in one run is finished there; the piece
+// with its first tile goes to the rows' own slot, a piece that begins inside a
+// segment to the CTA's (a run has one such piece at most, its first).
+// Warp (mt, kq) of the 4 MG math warps has m-tile mt (16 rows) and keys 16 kq
+// .. + 15 of every tile, and is alone in its loop: scores by mma.sync, a softmax of its own over its keys, P straight from the score
+// fragments into the second product.  (Sharing P through shared memory, with a
+// quarter of V's columns per warp, took two barriers and 2.5 times the
+// instructions per tile, and few_kernel ran at their latency, not memory's.)
+// At a segment's end the four key quarters are joined through the stage of its
+// last tile.  The last warp loads, running ahead over segments.
+// mma.sync, since so few rows would fill a small part of a tcgen05 tile, and
+// up to 48 rows memory bounds this kernel all the same.  Up to 16 rows the
+// tensor pipe has time to spare, and P goes in as two bf16 terms, P and its
+// rounding error, for two products; above rounded to bf16 once.
+template <int HD, int MG>
 struct Fw {
   static constexpr int TK = 64;                    // keys per tile
   static constexpr int KV = TK * HD * 2;           // bytes of K (or V) per stage
-  static constexpr int NST = HD == 128 ? 3 : 6;    // stages
-  static constexpr int PB = FEW * TK * 2;          // bytes of one term of P
-  static constexpr int SMEM = NST * 2 * KV + 2 * PB + 1024;
+  static constexpr int ROWS = 16 * MG;
+  static constexpr int NW = 4 * MG;                // math warps
+  static constexpr int THREADS = 32 * (NW + 1);
+  static constexpr int PER_SM = MG == 1 ? 3 : 1;   // CTAs that are resident together
+  static constexpr int NST = (MG == 1 ? 2 : 5) * (HD == 128 ? 1 : 2);  // stages
+  static constexpr bool LO = MG == 1;
+  static constexpr int QB = ROWS * HD * 2;
+  static constexpr int SMEM = NST * 2 * KV + QB + 1024;
 };
-constexpr int FW_THREADS = 160;
 
 // A sequence (or the prefix, b = batch) in the tile stream.
 struct FewSeq {
   Seq s;
-  int base;    // prefix: 0; own: P, the position of key 0
   int k_lo;    // first key that a row sees
   int k_end;   // keys
   int tiles;
 };
 __device__ __forceinline__ int few_tiles(const ShArgs& a, const Seq& s, int* k_lo) {
   *k_lo = a.window ? max(0, s.len - s.n - a.window + 1) : 0;
-  if (s.n == 0 || s.n * a.gq > FEW) return 0;
+  if (s.n == 0 || s.n * a.gq > a.few) return 0;
   return ((s.len + 63) >> 6) - (*k_lo >> 6);
 }
+// The prefix as a last sequence of all rows, when there are few; first_pos:
+// the lowest position of a row (INT_MAX: no rows).
+__device__ __forceinline__ int few_prefix_lo(const ShArgs& a, int first_pos) {
+  return a.window ? min(a.P, max(0, first_pos - a.window + 1)) : 0;
+}
+__device__ __forceinline__ int few_prefix_tiles(const ShArgs& a, int first_pos) {
+  if (!a.prefix_few || first_pos == 0x7fffffff) return 0;
+  const int lo = few_prefix_lo(a, first_pos);
+  return lo < a.P ? ((a.P + 63) >> 6) - (lo >> 6) : 0;
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void math_barrier() {
+  asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory");
+}
 
-template <int HD>
-__global__ void __launch_bounds__(FW_THREADS)
+// The stream's cut: W tiles in G runs (of a tile at least, so that the pieces
+// of a segment are those of consecutive CTAs), the first W % G one tile longer.
+struct Runs {
+  int G, q, r;
+  __device__ Runs(int W, int g) : G(min(g, max(W, 1))), q(W / G), r(W - q * G) {}
+  __device__ int begin(int c) const { return c * q + min(c, r); }
+  __device__ int of(int x) const { return x < r * (q + 1) ? x / (q + 1) : r + (x - r * (q + 1)) / q; }
+};
+
+template <int HD, int MG>
+__global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
     few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-               const __grid_constant__ ShArgs a) {
-  using C = Fw<HD>;
-  constexpr int NST = C::NST, KV = C::KV, PANELS = HD / 64, NT = HD / 32;  // NT: 8-column tiles of O per warp
+               const __grid_constant__ ShArgs a, const int lead) {
+  using C = Fw<HD, MG>;
+  constexpr int NST = C::NST, KV = C::KV, ROWS = C::ROWS, NT = HD / 8;
   extern __shared__ uint8_t fw_raw[];
   uint8_t* sm = fw_raw + ((1024u - (smem_addr(fw_raw) & 1023u)) & 1023u);
-  uint8_t* sP = sm + NST * 2 * KV;
-  int* cum = reinterpret_cast<int*>(sP + 2 * C::PB);  // [batch + 2]
+  uint8_t* sQ = sm + NST * 2 * KV;
+  int* cum = reinterpret_cast<int*>(sQ + C::QB);  // [batch + 2]
   __shared__ uint64_t full[NST], empty[NST];
-  __shared__ float s_max[4][FEW], s_sum[4][FEW];
-  __shared__ int s_warp[5], s_lo, s_first, s_bad;
-  __shared__ int s_abort;
+  __shared__ float2 s_ml[4][16];
+  __shared__ int s_vlo[ROWS], s_vhi[ROWS];
+  __shared__ int s_warp[C::NW + 1], s_lo, s_bad, s_abort;
   volatile int* abort_flag = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  launch_dependents();
   if (tid == 0) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(full + s, 1);
-      mbar_init(empty + s, 4);
+      mbar_init(empty + s, C::NW);
     }
     fence_mbar_init();
     s_abort = 0;
     s_lo = 0x7fffffff;
     s_bad = 0;
     cum[0] = 0;
-    tma_prefetch_map(&tmK);
-    tma_prefetch_map(&tmV);
   }
-  __syncthreads();
+  if (lead) wait_previous_kernel();  // as in tc_kernel
+  launch_dependents();
   // ---- the stream: tiles before each sequence ----
   int before = 0;
 #pragma unroll 1
-  for (int c0 = 0; c0 < a.batch; c0 += FW_THREADS) {
+  for (int c0 = 0; c0 < a.batch; c0 += C::THREADS) {
     int t = 0;
+    Seq s{0, 0, 0, 1};
     if (c0 + tid < a.batch) {
-      const Seq s = load_seq(a, c0 + tid);
+      s = load_seq(a, c0 + tid);
       int lo;
       t = few_tiles(a, s, &lo);
-      if (!s.ok) s_bad = 1;
-      if (s.n > 0) atomicMin(&s_lo, a.P + s.len - s.n);
     }
     int incl = t;
 #pragma unroll
@@ -740,38 +854,34 @@ __global__ void __launch_bounds__(FW_THREADS)
       const int u = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += u;
     }
+    __syncthreads();  // the initial values; the last round's s_warp has been read
+    if (!s.ok) s_bad = 1;
+    if (a.prefix_few && s.n > 0) atomicMin(&s_lo, a.P + s.len - s.n);
     if (lane == 31) s_warp[warp] = incl;
     __syncthreads();
     int off = before;
 #pragma unroll
-    for (int w = 0; w < 5; ++w) {
+    for (int w = 0; w < C::NW + 1; ++w) {
       if (w < warp) off += s_warp[w];
       before += s_warp[w];
     }
     if (c0 + tid < a.batch) cum[c0 + tid + 1] = off + incl;
-    __syncthreads();
   }
-  // the prefix as a last sequence of all rows, when there are few
-  int p_lo = 0;
-  if (a.prefix_few && s_lo != 0x7fffffff) {
-    p_lo = a.window ? min(a.P, max(0, s_lo - a.window + 1)) : 0;
-    if (p_lo < a.P) before += ((a.P + 63) >> 6) - (p_lo >> 6);
-  }
+  const int p_lo = few_prefix_lo(a, s_lo);
+  before += few_prefix_tiles(a, s_lo);
   if (tid == 0) cum[a.batch + 1] = before;
   __syncthreads();
-  if (blockIdx.x == 0) {
-    for (int i = tid; i < a.batch + 2; i += FW_THREADS) a.cum[i] = cum[i];
-    if (tid == 0 && s_bad) sh_error(a.err, EW_BAD_SHAPE);
-  }
-  const long long W = (long long)before * a.nkv;
-  const int x_lo = int(W * blockIdx.x / a.G), x_hi = int(W * (blockIdx.x + 1) / a.G);
+  if (blockIdx.x == 0 && tid == 0 && s_bad) sh_error(a.err, EW_BAD_SHAPE);
+  const Runs runs(before * a.nkv, a.G);
+  const int cta = int(blockIdx.x);
+  const int x_lo = cta < runs.G ? runs.begin(cta) : 0, x_hi = cta < runs.G ? min(runs.begin(cta + 1), before * a.nkv) : 0;
   // the sequence of the run's first tile
   int b0 = 0;
   {
     int hi = a.batch + 1;
     while (hi - b0 > 1) {
       const int mid = (b0 + hi) >> 1;
-      if ((long long)cum[mid] * a.nkv <= x_lo)
+      if (cum[mid] * a.nkv <= x_lo)
         b0 = mid;
       else
         hi = mid;
@@ -781,12 +891,10 @@ __global__ void __launch_bounds__(FW_THREADS)
     FewSeq f;
     if (b == a.batch) {
       f.s = Seq{0, total_rows(a), 0, 1};
-      f.base = 0;
       f.k_lo = p_lo;
       f.k_end = a.P;
     } else {
       f.s = load_seq(a, b);
-      f.base = a.P;
       few_tiles(a, f.s, &f.k_lo);
       f.k_end = f.s.len;
     }
@@ -794,7 +902,7 @@ __global__ void __launch_bounds__(FW_THREADS)
     return f;
   };
 
-  if (warp == 4) {
+  if (warp == C::NW) {
     // ---- loads ----
     uint32_t it = 0;
     bool ok = true;
@@ -819,8 +927,7 @@ __global__ void __launch_bounds__(FW_THREADS)
           }
         }
         const int kb = ((f.k_lo >> 6) + t + i) * 64;
-        if (lane == 0)
-          mbar_expect_tx(full + s, 2u * load_blocks<HD, 64>(kb, f.k_end, a.page_log2) * bs * HD * 2);
+        if (lane == 0) mbar_expect_tx(full + s, 2u * load_blocks<64>(kb, f.k_end, a.page_log2) * bs * HD * 2);
         __syncwarp();
         load_tile<HD, 64>(sm + s * 2 * KV, &tmK, pages, kb, f.k_end, kvh, full + s, a, lane);
         load_tile<HD, 64>(sm + s * 2 * KV + KV, &tmV, pages, kb, f.k_end, kvh, full + s, a, lane);
@@ -834,8 +941,16 @@ __global__ void __launch_bounds__(FW_THREADS)
     }
   } else {
     // ---- math ----
-    const int g = lane >> 2, tq = lane & 3;
-    uint32_t it = 0;
+    constexpr int NTH = C::NW * 32;
+    const int g = lane >> 2, tq = lane & 3, mi = lane >> 3, r7 = lane & 7;
+    const int kq = warp & 3, mt = warp >> 2;
+    // this lane's ldmatrix rows: a 16-byte chunk c of row r is at chunk c ^ (r
+    // & 7), so step ks (two chunks) flips bits 5 and 6 of the address
+    const uint32_t k_off = (16 * kq + (mi >> 1) * 8 + r7) * 128 + (((mi & 1) ^ r7) << 4);
+    const uint32_t v_off = (16 * kq + (mi & 1) * 8 + r7) * 128 + (((mi >> 1) ^ r7) << 4);
+    const uint32_t q_at = smem_addr(sQ) + (16 * mt + (mi & 1) * 8 + r7) * 128 + (((mi >> 1) ^ r7) << 4);
+    const uint32_t ring = smem_addr(sm);
+    uint32_t st = 0, phase = 0;
     int b = b0;
     bool ok = true;
 #pragma unroll 1
@@ -844,62 +959,60 @@ __global__ void __launch_bounds__(FW_THREADS)
       const FewSeq f = seq_at(b);
       const int y = x - cum[b] * a.nkv, kvh = y / f.tiles, t0 = y - kvh * f.tiles;
       const int nt = min(x_hi - x, f.tiles - t0);
-      // packed rows g and g + 8 of the segment: tokens, heads, visible keys
-      int tok[2], head[2], vlo[2], vhi[2];
-      bool live[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int pr = g + 8 * e;
-        live[e] = pr < f.s.n * a.gq;
-        const int i = live[e] ? pr / a.gq : 0;
-        tok[e] = f.s.r0 + i;
-        head[e] = kvh * a.gq + (live[e] ? pr - i * a.gq : 0);
-        vlo[e] = vhi[e] = 0;
-        if (live[e]) {
+      const int nrow = f.s.n * a.gq, nmt = (nrow + 15) >> 4;
+      // ---- Q into shared memory (128-byte swizzle; zero rows up to whole
+      // m-tiles), each row's visible keys beside it ----
+      for (int i = tid; i < nmt * 16 * (HD / 8); i += NTH) {
+        const int row = i / (HD / 8), c = i - row * (HD / 8);
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (row < nrow) {
+          const int tok = row / a.gq;
+          q = *reinterpret_cast<const uint4*>(
+              a.q + ((size_t)(f.s.r0 + tok) * a.nq + kvh * a.gq + (row - tok * a.gq)) * HD + c * 8);
+        }
+        *reinterpret_cast<uint4*>(sQ + (c >> 3) * (ROWS * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = q;
+      }
+      if (tid < nmt * 16) {
+        int vlo = 0, vhi = 0;
+        if (tid < nrow) {
+          const int i = tid / a.gq;
           if (b == a.batch) {
-            vhi[e] = a.P;
+            vhi = a.P;
             if (a.window) {
               int lo = 0, hi = a.batch;
               while (hi - lo > 1) {
                 const int mid = (lo + hi) >> 1;
-                if (a.row_start[mid] <= tok[e])
+                if (a.row_start[mid] <= i)
                   lo = mid;
                 else
                   hi = mid;
               }
               const Seq s = load_seq(a, lo);
-              vlo[e] = s.n ? min(a.P, max(0, a.P + s.len - s.n + (tok[e] - s.r0) - a.window + 1)) : a.P;
+              vlo = s.n ? min(a.P, max(0, a.P + s.len - s.n + (i - s.r0) - a.window + 1)) : a.P;
             }
           } else {
             const int p = f.s.len - f.s.n + i;
-            vhi[e] = p + 1;
-            if (a.window) vlo[e] = max(0, p - a.window + 1);
+            vhi = p + 1;
+            if (a.window) vlo = max(0, p - a.window + 1);
           }
         }
+        s_vlo[tid] = vlo;
+        s_vhi[tid] = vhi;
       }
-      // Q as A fragments
-      uint32_t qf[HD / 16][4];
+      math_barrier<NTH>();
+      // keys that every row sees lie in [in_lo, in_hi)
+      const int in_lo = b == a.batch ? (a.window ? a.P : 0) : (a.window ? max(0, f.s.len - a.window) : 0);
+      const int in_hi = b == a.batch ? a.P : f.s.len - f.s.n + 1;
+      float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-      for (int ks = 0; ks < HD / 16; ++ks) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int rr = e & 1;
-          const size_t at = ((size_t)tok[rr] * a.nq + head[rr]) * HD + ks * 16 + (e >> 1) * 8 + 2 * tq;
-          qf[ks][e] = live[rr] ? *reinterpret_cast<const uint32_t*>(a.q + at) : 0u;
-        }
-      }
-      float o[NT][4];
-#pragma unroll
-      for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-      float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+      for (int c = 0; c < NT; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
+      const bool busy = mt < nmt;
 #pragma unroll 1
-      for (int i = 0; i < nt; ++i, ++it) {
-        const int st = int(it % NST);
-        if (!__all_sync(0xffffffffu, sh_wait(full + st, (it / NST) & 1u, abort_flag, a.err))) ok = false;
+      for (int i = 0; i < nt; ++i) {
         // (on a failed wait the warps still meet at the barriers below)
-        const uint8_t* sK = sm + st * 2 * KV;
-        uint8_t* sV = sm + st * 2 * KV + KV;
-        const int kb = ((f.k_lo >> 6) + t0 + i) * 64, k0 = kb + 16 * warp;
+        if (!__all_sync(0xffffffffu, sh_wait(full + st, phase, abort_flag, a.err))) ok = false;
+        const uint32_t sK = ring + st * 2 * KV, sV = sK + KV;
+        const int kb = ((f.k_lo >> 6) + t0 + i) * 64, k0 = kb + 16 * kq;
         if (kb < f.k_lo || kb + 64 > f.k_end) {
           // values that no row sees must be finite (0 x NaN): clear them
           const int row = lane >> 1, key = k0 + row;
@@ -907,131 +1020,150 @@ __global__ void __launch_bounds__(FW_THREADS)
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c) {
               const int ch = (lane & 1) * (HD / 16) + c;
-              *reinterpret_cast<uint4*>(sV + (ch >> 3) * (64 * 128) + (16 * warp + row) * 128 + ((ch & 7) << 4)) =
-                  make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(sm + st * 2 * KV + KV + (ch >> 3) * (64 * 128) + (16 * kq + row) * 128 +
+                                        ((ch & 7) << 4)) = make_uint4(0u, 0u, 0u, 0u);
             }
           }
           fence_proxy_async();  // before the stage is refilled
+          __syncwarp();
         }
-        float s[2][4] = {};
+        if (busy) {
+          float s[2][4] = {};
 #pragma unroll
-        for (int ks = 0; ks < HD / 16; ++ks) {
-          const int mi = lane >> 3, key = 16 * warp + (mi >> 1) * 8 + (lane & 7), ch = 2 * ks + (mi & 1);
-          uint32_t k0r, k1r, k2r, k3r;
-          ldsm_x4(k0r, k1r, k2r, k3r, sK + (ch >> 3) * (64 * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
-          mma_16816(s[0], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], k0r, k1r);
-          mma_16816(s[1], qf[ks][0], qf[ks][1], qf[ks][2], qf[ks][3], k2r, k3r);
-        }
-        float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = k0 + j * 8 + 2 * tq + (e & 1), rr = e >> 1;
-            s[j][e] = (key >= vlo[rr] && key < vhi[rr]) ? s[j][e] * a.scale_log2 : -INFINITY;
-            mx[rr] = fmaxf(mx[rr], s[j][e]);
+          for (int ks = 0; ks < HD / 16; ++ks) {
+            uint32_t kf[4], qf[4];
+            ldsm4(kf, ((sK + k_off) ^ ((ks & 3) << 5)) + (ks >> 2) * (64 * 128));
+            ldsm4(qf, (q_at ^ ((ks & 3) << 5)) + (ks >> 2) * (ROWS * 128));
+            mma_16816(s[0], qf[0], qf[1], qf[2], qf[3], kf[0], kf[1]);
+            mma_16816(s[1], qf[0], qf[1], qf[2], qf[3], kf[2], kf[3]);
           }
-#pragma unroll
-        for (int off = 1; off <= 2; off <<= 1) {
-          mx[0] = fmaxf(mx[0], __shfl_xor_sync(0xffffffffu, mx[0], off));
-          mx[1] = fmaxf(mx[1], __shfl_xor_sync(0xffffffffu, mx[1], off));
-        }
-        if (tq == 0) {
-          s_max[warp][g] = mx[0];
-          s_max[warp][g + 8] = mx[1];
-        }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        float nref[2];
-#pragma unroll
-        for (int rr = 0; rr < 2; ++rr) {
-          float M = -INFINITY;
-#pragma unroll
-          for (int w = 0; w < 4; ++w) M = fmaxf(M, s_max[w][g + 8 * rr]);
-          if (M > m[rr] + RESCALE) {
-            const float al = exp2f(m[rr] - M);
-            m[rr] = M;
-            l[rr] *= al;
-#pragma unroll
-            for (int c = 0; c < NT; ++c) {
-              o[c][2 * rr] *= al;
-              o[c][2 * rr + 1] *= al;
-            }
-          }
-          nref[rr] = m[rr] == -INFINITY ? 0.f : m[rr];
-        }
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
+          const bool edge = kb < in_lo || kb + 64 > in_hi;
+          uint32_t ph[4], pl[4];
 #pragma unroll
           for (int rr = 0; rr < 2; ++rr) {
-            const float p0 = ex2_fast(s[j][2 * rr] - nref[rr]), p1 = ex2_fast(s[j][2 * rr + 1] - nref[rr]);
-            l[rr] += p0 + p1;
-            uint32_t hi, lo;
-            split_bf16x2(p0, p1, hi, lo);
-            const int row = g + 8 * rr, ch = 2 * warp + j;
-            uint8_t* d = sP + row * 128 + ((ch ^ (row & 7)) << 4) + 4 * tq;
-            *reinterpret_cast<uint32_t*>(d) = hi;
-            *reinterpret_cast<uint32_t*>(d + C::PB) = lo;
+            float z0 = s[0][2 * rr], z1 = s[0][2 * rr + 1], z2 = s[1][2 * rr], z3 = s[1][2 * rr + 1];
+            if (edge) {
+              const int row = 16 * mt + g + 8 * rr, lo = s_vlo[row] - k0 - 2 * tq, hi = s_vhi[row] - k0 - 2 * tq;
+              z0 = (0 >= lo && 0 < hi) ? z0 : -INFINITY;
+              z1 = (1 >= lo && 1 < hi) ? z1 : -INFINITY;
+              z2 = (8 >= lo && 8 < hi) ? z2 : -INFINITY;
+              z3 = (9 >= lo && 9 < hi) ? z3 : -INFINITY;
+            }
+            float M = fmaxf(fmaxf(z0, z1), fmaxf(z2, z3));
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 1));
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 2)) * a.scale_log2;
+            if (M > m[rr] + RESCALE) {
+              const float al = exp2f(m[rr] - M);
+              m[rr] = M;
+              l[rr] *= al;
+#pragma unroll
+              for (int c = 0; c < NT; ++c) {
+                o[c][2 * rr] *= al;
+                o[c][2 * rr + 1] *= al;
+              }
+            }
+            const float nref = m[rr] == -INFINITY ? 0.f : -m[rr];
+            const float p0 = ex2_fast(fmaf(z0, a.scale_log2, nref)), p1 = ex2_fast(fmaf(z1, a.scale_log2, nref));
+            const float p2 = ex2_fast(fmaf(z2, a.scale_log2, nref)), p3 = ex2_fast(fmaf(z3, a.scale_log2, nref));
+            l[rr] += (p0 + p1) + (p2 + p3);
+            const uint32_t h0 = cvt_bf16x2(p0, p1), h1 = cvt_bf16x2(p2, p3);
+            ph[rr] = h0;
+            ph[2 + rr] = h1;
+            if (C::LO) {
+              pl[rr] = cvt_bf16x2(p0 - __uint_as_float(h0 << 16), p1 - __uint_as_float(h0 & 0xffff0000u));
+              pl[2 + rr] = cvt_bf16x2(p2 - __uint_as_float(h1 << 16), p3 - __uint_as_float(h1 & 0xffff0000u));
+            }
           }
-        asm volatile("bar.sync 1, 128;" ::: "memory");
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-          const int mi = lane >> 3;
-          const int prow = (mi & 1) * 8 + (lane & 7), pch = 2 * ks + (mi >> 1);
-          uint32_t h0, h1, h2, h3, e0, e1, e2, e3;
-          const uint8_t* pp = sP + prow * 128 + ((pch ^ (prow & 7)) << 4);
-          ldsm_x4(h0, h1, h2, h3, pp);
-          ldsm_x4(e0, e1, e2, e3, pp + C::PB);
-          const int key = ks * 16 + (mi & 1) * 8 + (lane & 7);
-#pragma unroll
-          for (int c = 0; c < NT; c += 2) {
-            const int ch = warp * NT + c + (mi >> 1);
-            uint32_t v0, v1, v2, v3;
-            ldsm_x4_t(v0, v1, v2, v3, sV + (ch >> 3) * (64 * 128) + key * 128 + (((ch & 7) ^ (key & 7)) << 4));
-            mma_16816(o[c], h0, h1, h2, h3, v0, v1);
-            mma_16816(o[c], e0, e1, e2, e3, v0, v1);
-            mma_16816(o[c + 1], h0, h1, h2, h3, v2, v3);
-            mma_16816(o[c + 1], e0, e1, e2, e3, v2, v3);
+          for (int p = 0; p < HD / 16; ++p) {
+            uint32_t vf[4];
+            ldsm4_t(vf, ((sV + v_off) ^ ((p & 3) << 5)) + (p >> 2) * (64 * 128));
+            mma_16816(o[2 * p], ph[0], ph[1], ph[2], ph[3], vf[0], vf[1]);
+            mma_16816(o[2 * p + 1], ph[0], ph[1], ph[2], ph[3], vf[2], vf[3]);
+            if (C::LO) {
+              mma_16816(o[2 * p], pl[0], pl[1], pl[2], pl[3], vf[0], vf[1]);
+              mma_16816(o[2 * p + 1], pl[0], pl[1], pl[2], pl[3], vf[2], vf[3]);
+            }
           }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + st);
+        if (i + 1 < nt) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(empty + st);
+          if (++st == NST) {
+            st = 0;
+            phase ^= 1;
+          }
+        }
       }
-      // ---- the piece's sums: over the quad, then over the warps ----
-#pragma unroll
-      for (int off = 1; off <= 2; off <<= 1) {
-        l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
-        l[1] += __shfl_xor_sync(0xffffffffu, l[1], off);
-      }
-      if (tq == 0) {
-        s_sum[warp][g] = l[0];
-        s_sum[warp][g + 8] = l[1];
-      }
-      asm volatile("bar.sync 1, 128;" ::: "memory");
+      // ---- the piece: the four key quarters of each m-tile joined through
+      // the last tile's stage, [quarter][16 rows][HD] fp32 (16-byte chunks
+      // flipped by the row), a warp then writing whole rows ----
+      float* sx = reinterpret_cast<float*>(sm + st * 2 * KV);
+      const bool first = t0 == 0, whole = first && nt == f.tiles && b < a.batch && a.ns_prefix == 0;
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
-        const int row = g + 8 * rr;
-        float L = 0.f;
+        l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
+        l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
+      }
+#pragma unroll 1
+      for (int jt = 0; jt < nmt; ++jt) {
+        math_barrier<NTH>();  // the stage has been read; the last round is over
+        if (jt == mt) {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) L += s_sum[w][row];
-        if (!live[rr] || !ok) continue;
-        const bool first = t0 == 0, whole = first && nt == f.tiles;
-        if (whole && b < a.batch && a.ns_prefix == 0) {
-          const float inv = L > 0.f ? 1.f / L : 0.f;
-          uint16_t* dst = a.out + ((size_t)tok[rr] * a.nq + head[rr]) * HD + warp * NT * 8 + 2 * tq;
+          for (int rr = 0; rr < 2; ++rr) {
+            const int row = g + 8 * rr;
+            float* d = sx + (kq * 16 + row) * HD;
 #pragma unroll
-          for (int c = 0; c < NT; ++c)
-            *reinterpret_cast<uint32_t*>(dst + 8 * c) = cvt_bf16x2(o[c][2 * rr] * inv, o[c][2 * rr + 1] * inv);
-        } else {
-          const size_t at = first ? ((size_t)(b == a.batch ? 0 : a.ns_prefix) * a.rows + tok[rr]) * a.nq + head[rr]
-                                  : (size_t)blockIdx.x * FEW + row;
-          float* dst = (first ? a.o_part : a.o_cont) + at * HD + warp * NT * 8 + 2 * tq;
+            for (int c = 0; c < NT; ++c)
+              *reinterpret_cast<float2*>(d + ((8 * c + 2 * tq) ^ ((row & 7) << 2))) =
+                  make_float2(o[c][2 * rr], o[c][2 * rr + 1]);
+            if (tq == 0) s_ml[kq][row] = make_float2(m[rr], l[rr]);
+          }
+        }
+        math_barrier<NTH>();
+        constexpr int CPR = HD / 4;  // 16-byte chunks of a row
+        const int items = min(16, nrow - 16 * jt) * CPR;
+#pragma unroll 2
+        for (int it = tid; it < items; it += NTH) {
+          const int row = it / CPR, c4 = it - row * CPR;
+          float2 ml[4];
+          float4 x[4];
 #pragma unroll
-          for (int c = 0; c < NT; ++c)
-            *reinterpret_cast<float2*>(dst + 8 * c) = make_float2(o[c][2 * rr], o[c][2 * rr + 1]);
-          if (warp == 0 && tq == 0) (first ? a.ml_part : a.ml_cont)[at] = make_float2(m[rr], L);
+          for (int k = 0; k < 4; ++k) {
+            ml[k] = s_ml[k][row];
+            x[k] = *reinterpret_cast<const float4*>(sx + (k * 16 + row) * HD + ((c4 * 4) ^ ((row & 7) << 2)));
+          }
+          const float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
+          float L = 0.f;
+          float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float f = ml[k].x == -INFINITY ? 0.f : exp2f(ml[k].x - M);
+            L = fmaf(ml[k].y, f, L);
+            y = make_float4(fmaf(x[k].x, f, y.x), fmaf(x[k].y, f, y.y), fmaf(x[k].z, f, y.z), fmaf(x[k].w, f, y.w));
+          }
+          if (!ok) continue;
+          const int pr = 16 * jt + row, tk = pr / a.gq;
+          const size_t line = (size_t)(f.s.r0 + tk) * a.nq + kvh * a.gq + (pr - tk * a.gq);
+          if (whole) {
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            *reinterpret_cast<uint2*>(a.out + line * HD + c4 * 4) =
+                make_uint2(cvt_bf16x2(y.x * inv, y.y * inv), cvt_bf16x2(y.z * inv, y.w * inv));
+          } else {
+            const size_t at = first ? (size_t)(b == a.batch ? 0 : a.ns_prefix) * a.rows * a.nq + line
+                                    : (size_t)cta * a.few + pr;
+            *reinterpret_cast<float4*>((first ? a.o_part : a.o_cont) + at * HD + c4 * 4) = y;
+            if (c4 == 0) (first ? a.ml_part : a.ml_cont)[at] = make_float2(M, L);
+          }
         }
       }
-      asm volatile("bar.sync 1, 128;" ::: "memory");  // s_sum is free again
+      fence_proxy_async();  // the stage is refilled by tensor copies
+      math_barrier<NTH>();  // and the rows' bounds and Q are free again
+      if (lane == 0) mbar_arrive(empty + st);
+      if (++st == NST) {
+        st = 0;
+        phase ^= 1;
+      }
       x += nt;
     }
   }
@@ -1039,99 +1171,137 @@ __global__ void __launch_bounds__(FW_THREADS)
 }
 
 // ---------------------------------------------------------------------------
-// join_kernel: one CTA per token, one warp per head at a time
+// join_kernel: CTA = one head and `tpc` tokens, a warp per token at a time.
+// Where a token's pieces are is worked out before the wait for them (the
+// stream's cut again, from the lengths), while they are still being made;
+// behind the wait there is one round of loads per eight pieces, (m, l) and O
+// together.
 // ---------------------------------------------------------------------------
-constexpr int JT = 256;
+constexpr int JT = 256, JCH = 8;
 
 template <int HD>
-__global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs a) {
-  __shared__ int s_b;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, tok = blockIdx.x;
-  if (tid == 0) s_b = -1;
+__global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs a, const int tpc) {
+  extern __shared__ int s_start[];        // row_start [batch + 1], then the stream's tiles before each sequence
+  int* cum = s_start + a.batch + 1;       // [batch + 2]
+  __shared__ int s_warp[JT / 32], s_lo;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int head = blockIdx.y, kvh = head / a.gq, g = head - kvh * a.gq;
+  if (tid == 0) {
+    cum[0] = 0;
+    s_lo = 0x7fffffff;
+    s_start[a.batch] = a.row_start[a.batch];
+  }
   __syncthreads();
-  for (int b = tid; b < a.batch; b += JT)
-    if (a.row_start[b] <= tok && tok < a.row_start[b + 1]) s_b = b;
-  __syncthreads();
-  const int b = s_b;
-  wait_previous_kernel();
-  if (b < 0) return;
-  const Seq s = load_seq(a, b);
-  if (tok < s.r0 || tok >= s.r0 + s.n) return;
-  const bool few = s.n * a.gq <= FEW;
-  const int local = (tok - s.r0) * a.gq;
-  const int tiles = few ? a.cum[b + 1] - a.cum[b] : 0, x0 = few ? a.cum[b] * a.nkv : 0;
-  const int ptiles = a.prefix_few ? a.cum[a.batch + 1] - a.cum[a.batch] : 0, px0 = a.prefix_few ? a.cum[a.batch] * a.nkv : 0;
-  const long long W = (long long)a.cum[a.batch + 1] * a.nkv;
-  auto cta_of = [&](long long x) { return int(((x + 1) * a.G - 1) / W); };  // of the run that holds tile x
-  constexpr int E = HD / 32;
-  for (int head = warp; head < a.nq; head += JT / 32) {
-    const int kvh = head / a.gq, g = head - kvh * a.gq;
-    // the pieces: slots [first, n_slots), then the CTAs [c0, c1) of the own positions and [p0, p1) of the prefix
-    int n_slots = a.ns_prefix + (few ? 1 : a.ns_own), first = 0, c0 = 0, nc = 0, p0 = 0, np = 0;
+  int before = 0;
+#pragma unroll 1
+  for (int c0 = 0; c0 < a.batch; c0 += JT) {
+    int t = 0;
+    if (c0 + tid < a.batch) {
+      const Seq s = load_seq(a, c0 + tid);
+      int lo;
+      t = few_tiles(a, s, &lo);
+      s_start[c0 + tid] = s.r0;
+      if (a.prefix_few && s.n > 0) atomicMin(&s_lo, a.P + s.len - s.n);
+    }
+    int incl = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    if (lane == 31) s_warp[warp] = incl;
+    __syncthreads();
+    int off = before;
+#pragma unroll
+    for (int w = 0; w < JT / 32; ++w) {
+      if (w < warp) off += s_warp[w];
+      before += s_warp[w];
+    }
+    if (c0 + tid < a.batch) cum[c0 + tid + 1] = off + incl;
+    __syncthreads();
+  }
+  const int ptiles = few_prefix_tiles(a, s_lo), px = before * a.nkv + kvh * ptiles;
+  const Runs runs((before + ptiles) * a.nkv, a.G);
+  bool waited = false;
+  const int tok1 = min(a.rows, int(blockIdx.x + 1) * tpc);
+  for (int tok = blockIdx.x * tpc + warp; tok < tok1; tok += JT / 32) {
+    int b = 0, hi = a.batch;
+    while (hi - b > 1) {
+      const int mid = (b + hi) >> 1;
+      if (s_start[mid] <= tok)
+        b = mid;
+      else
+        hi = mid;
+    }
+    const Seq s = load_seq(a, b);
+    if (tok < s.r0 || tok >= s.r0 + s.n) continue;
+    const bool few = s.n * a.gq <= a.few;
+    if (!few && a.own_joins) continue;  // finished by tc_kernel
+    // the pieces: slots [first, first + in_slots), then the CTAs [c0, c0 + nc)
+    // of the own positions and [p0, p0 + np) of the prefix
+    int first = 0, in_slots = a.ns_prefix + (few ? 1 : a.ns_own), c0 = 0, nc = 0, p0 = 0, np = 0;
     if (few) {
-      const long long x = x0 + (long long)kvh * tiles;
-      c0 = cta_of(x) + 1;
-      nc = cta_of(x + tiles - 1) + 1 - c0;
+      const int tiles = cum[b + 1] - cum[b], x = cum[b] * a.nkv + kvh * tiles;
+      c0 = runs.of(x) + 1;
+      nc = runs.of(x + tiles - 1) + 1 - c0;
       if (a.ns_prefix == 0 && nc == 0) continue;  // written already
-    } else if (a.ns_prefix == 0 && a.ns_own == 1) {
-      continue;
     }
     if (a.prefix_few) {
       if (ptiles == 0) {
         first = 1;  // the window ends behind the prefix: slot 0 was not written
+        --in_slots;
       } else {
-        const long long x = px0 + (long long)kvh * ptiles;
-        p0 = cta_of(x) + 1;
-        np = cta_of(x + ptiles - 1) + 1 - p0;
+        p0 = runs.of(px) + 1;
+        np = runs.of(px + ptiles - 1) + 1 - p0;
       }
     }
-    const int total = (n_slots - first) + nc + np;
-    auto piece = [&](int i, const float*& o, float2& ml) {
-      if (i < n_slots - first) {
-        const size_t at = ((size_t)(first + i) * a.rows + tok) * a.nq + head;
-        o = a.o_part + at * HD;
-        ml = a.ml_part[at];
-      } else {
-        i -= n_slots - first;
-        const bool mine = i < nc;
-        const size_t at = (size_t)(mine ? c0 + i : p0 + i - nc) * FEW + (mine ? local : tok * a.gq) + g;
-        o = a.o_cont + at * HD;
-        ml = a.ml_cont[at];
+    const int total = in_slots + nc + np, crow = (tok - s.r0) * a.gq + g, prow = tok * a.gq + g;
+    const size_t line = (size_t)tok * a.nq + head;
+    if (!waited) wait_previous_kernel();
+    waited = true;
+    constexpr int E = HD / 32;
+    float acc[E] = {}, L = 0.f, M = -INFINITY;
+#pragma unroll 1
+    for (int i0 = 0; i0 < total; i0 += JCH) {
+      float2 ml[JCH];
+      float x[JCH][E];
+#pragma unroll
+      for (int k = 0; k < JCH; ++k) {
+        const int i = min(i0 + k, total - 1);
+        const bool slot = i < in_slots, mine = i < in_slots + nc;
+        const size_t at = slot ? (size_t)(first + i) * a.rows * a.nq + line
+                               : (size_t)(mine ? c0 + i - in_slots : p0 + i - in_slots - nc) * a.few + (mine ? crow : prow);
+        ml[k] = (slot ? a.ml_part : a.ml_cont)[at];
+        const float* src = (slot ? a.o_part : a.o_cont) + at * HD + lane * E;
+        if (E == 4)
+          *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(src);
+        if (i0 + k >= total) ml[k].y = 0.f;
       }
-    };
-    float M = -INFINITY;
-    for (int i = lane; i < total; i += 32) {
-      const float* o;
-      float2 ml;
-      piece(i, o, ml);
-      if (ml.y > 0.f) M = fmaxf(M, ml.x);
-    }
+      float m = M;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float acc[E] = {}, L = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < total; ++i) {
-      const float* o;
-      float2 ml;
-      piece(i, o, ml);
-      if (ml.y > 0.f) {
-        const float f = exp2f(ml.x - M);
-        L = fmaf(ml.y, f, L);
-        const float* src = o + lane * E;
+      for (int k = 0; k < JCH; ++k) m = ml[k].y > 0.f ? fmaxf(m, ml[k].x) : m;
+      const float f = M == -INFINITY ? 0.f : exp2f(M - m);
+      M = m;
+      L *= f;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(src + e);
-          acc[e] = fmaf(v.x, f, acc[e]);
-          acc[e + 1] = fmaf(v.y, f, acc[e + 1]);
-        }
+      for (int e = 0; e < E; ++e) acc[e] *= f;
+#pragma unroll
+      for (int k = 0; k < JCH; ++k) {
+        if (!(ml[k].y > 0.f)) continue;  // an empty piece's O was not written
+        const float w = exp2f(ml[k].x - M);
+        L = fmaf(ml[k].y, w, L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(x[k][e], w, acc[e]);
       }
     }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    uint16_t* dst = a.out + ((size_t)tok * a.nq + head) * HD + lane * E;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + line * HD + lane * E);
 #pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(dst + e) = cvt_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < E; e += 2) dst[e / 2] = cvt_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   }
+  if (!waited) wait_previous_kernel();
 }
 
 // ---------------------------------------------------------------------------
@@ -1185,7 +1355,8 @@ int pieces_for(long long items, int tiles, int sms, int cap) {
 }
 
 struct ShPlan {
-  bool many;              // some sequence may have more than FEW packed rows
+  int few;                // packed rows of a sequence that few_kernel takes
+  bool many;              // some sequence may have more
   bool tc_prefix_alt, tc_own_alt;
   long long prefix_items, own_items;
   int prefix_cap, own_cap;
@@ -1197,13 +1368,14 @@ ShPlan shared_plan(int rows, int batch, int nq, int nkv, int max_new, int sms) {
   ShPlan p;
   const long long packed = (long long)rows * gq;
   const long long most = (long long)(max_new < rows ? max_new : rows) * gq;  // packed rows of one sequence
-  p.many = most > FEW;
+  p.few = most <= 16 ? 16 : (most <= 32 ? 32 : MAX_FEW);
+  p.many = most > p.few;
   p.tc_prefix_alt = packed <= 128;
   p.tc_own_alt = most <= 128;
   p.prefix_items = nkv * ((packed + (p.tc_prefix_alt ? 127 : 255)) / (p.tc_prefix_alt ? 128 : 256));
   // tiles of the sequences with many rows: at most one partly filled tile each
   const long long tr = p.tc_own_alt ? 128 : 256;
-  long long seqs = packed / (FEW + 1) + 1;
+  long long seqs = packed / (p.few + 1) + 1;
   if (seqs > batch) seqs = batch;
   p.own_items = nkv * (packed / tr + seqs);
   auto cap = [&](long long items) {
@@ -1212,29 +1384,30 @@ ShPlan shared_plan(int rows, int batch, int nq, int nkv, int max_new, int sms) {
   };
   p.prefix_cap = cap(p.prefix_items);
   p.own_cap = p.many ? cap(p.own_items) : 1;
-  p.G = 2 * sms;
+  p.G = (p.few == 16 ? Fw<128, 1>::PER_SM : 1) * sms;  // CTAs that are resident together
   return p;
 }
 
 struct ShLayout {
-  size_t cum, ml_part, ml_cont, o_cont, o_part, total;
+  size_t ml_part, ml_cont, o_cont, o_part, total;
 };
-ShLayout shared_layout(const ShPlan& p, int rows, int batch, int nq, int hd) {
+ShLayout shared_layout(const ShPlan& p, int rows, int nq, int hd) {
   auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
   ShLayout L;
   const size_t parts = p.prefix_cap + p.own_cap, lines = parts * rows * nq;
-  L.cum = 256;
-  L.ml_part = L.cum + al((size_t)(batch + 2) * 4);
+  L.ml_part = 256;
   L.ml_cont = L.ml_part + al(lines * 8);
-  L.o_cont = L.ml_cont + al((size_t)p.G * FEW * 8);
-  L.o_part = L.o_cont + al((size_t)p.G * FEW * hd * 4);
+  L.o_cont = L.ml_cont + al((size_t)p.G * p.few * 8);
+  L.o_part = L.o_cont + al((size_t)p.G * p.few * hd * 4);
   L.total = L.o_part + al(lines * hd * 4);
   return L;
 }
 
-cudaError_t launch(const void* fn, unsigned grid, unsigned threads, int smem, bool after, void** args, cudaStream_t st) {
+// Every launch may start before the one in front of it in the stream has
+// finished (the kernels wait for it where they need it).
+cudaError_t launch(const void* fn, dim3 grid, unsigned threads, int smem, void** args, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = size_t(smem);
   cfg.stream = st;
@@ -1242,7 +1415,7 @@ cudaError_t launch(const void* fn, unsigned grid, unsigned threads, int smem, bo
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = after ? 1 : 0;
+  cfg.numAttrs = 1;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1263,32 +1436,42 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
   }
   if ((e = page_map(&k64, k, HD, page, blocks, page < 64 ? page : 64)) != cudaSuccess) return e;
   if ((e = page_map(&v64, v, HD, page, blocks, page < 64 ? page : 64)) != cudaSuccess) return e;
-  bool after = false;
+  int lead = 1;  // the call's first launch
   for (int own = 0; own < 2; ++own) {
     if (own ? !p.many : !tc_prefix) continue;
     const bool alt = own ? p.tc_own_alt : p.tc_prefix_alt;
     const long long items = (own ? p.own_items : p.prefix_items) * (own ? a.ns_own : a.ns_prefix);
-    void* args[] = {&k128, &v128, &a, &own};
+    void* args[] = {&k128, &v128, &a, &own, &lead};
     const void* fn = alt ? reinterpret_cast<const void*>(&tc_kernel<HD, true>)
                          : reinterpret_cast<const void*>(&tc_kernel<HD, false>);
-    e = launch(fn, unsigned(items), TC_THREADS, alt ? Tc<HD, true>::SMEM : Tc<HD, false>::SMEM, after, args, st);
+    e = launch(fn, dim3(unsigned(items)), TC_THREADS, alt ? Tc<HD, true>::SMEM : Tc<HD, false>::SMEM, args, st);
     if (e != cudaSuccess) return e;
-    after = true;
+    lead = 0;
   }
   {
-    void* args[] = {&k64, &v64, &a};
-    e = launch(reinterpret_cast<const void*>(&few_kernel<HD>), unsigned(a.G), FW_THREADS,
-               Fw<HD>::SMEM + ((a.batch + 2) * 4 + 15) / 16 * 16, after, args, st);
+    void* args[] = {&k64, &v64, &a, &lead};
+    using F1 = Fw<HD, 1>;
+    using F2 = Fw<HD, 2>;
+    using F3 = Fw<HD, 3>;
+    const void* fn = p.few == 16   ? reinterpret_cast<const void*>(&few_kernel<HD, 1>)
+                     : p.few == 32 ? reinterpret_cast<const void*>(&few_kernel<HD, 2>)
+                                   : reinterpret_cast<const void*>(&few_kernel<HD, 3>);
+    const int smem = p.few == 16 ? F1::SMEM : (p.few == 32 ? F2::SMEM : F3::SMEM);
+    const int threads = p.few == 16 ? F1::THREADS : (p.few == 32 ? F2::THREADS : F3::THREADS);
+    e = launch(fn, dim3(unsigned(a.G)), threads, smem + ((a.batch + 2) * 4 + 15) / 16 * 16, args, st);
     if (e != cudaSuccess) return e;
   }
-  void* args[] = {&a};
-  return launch(reinterpret_cast<const void*>(&join_kernel<HD>), unsigned(a.rows), JT, 0, true, args, st);
+  // tokens per CTA of the join: one a warp when few, more where most CTAs may find nothing to do
+  int tpc = a.rows <= 256 ? 8 : 64;
+  void* args[] = {&a, &tpc};
+  return launch(reinterpret_cast<const void*>(&join_kernel<HD>),
+                dim3(unsigned((a.rows + tpc - 1) / tpc), unsigned(a.nq)), JT, (2 * a.batch + 3) * 4, args, st);
 }
 
 }  // namespace
 
 size_t attn_shared_ws(int rows, int batch, int nq, int nkv, int hd, int max_new, int sms) {
-  return shared_layout(shared_plan(rows, batch, nq, nkv, max_new, sms), rows, batch, nq, hd).total;
+  return shared_layout(shared_plan(rows, batch, nq, nkv, max_new, sms), rows, nq, hd).total;
 }
 
 cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, int nkv, int hd, const uint16_t* k,
@@ -1296,7 +1479,7 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
                                const int32_t* table, int width, const int32_t* ptable, int P, int window, int max_new,
                                uint16_t* out, uint8_t* ws, int sms, cudaStream_t st) {
   const ShPlan p = shared_plan(rows, batch, nq, nkv, max_new, sms);
-  const ShLayout L = shared_layout(p, rows, batch, nq, hd);
+  const ShLayout L = shared_layout(p, rows, nq, hd);
   ShArgs a;
   a.q = q;
   a.row_start = row_start;
@@ -1305,7 +1488,6 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
   a.ptable = ptable;
   a.out = out;
   a.err = reinterpret_cast<uint32_t*>(ws) + 2;
-  a.cum = reinterpret_cast<int32_t*>(ws + L.cum);
   a.ml_part = reinterpret_cast<float2*>(ws + L.ml_part);
   a.ml_cont = reinterpret_cast<float2*>(ws + L.ml_cont);
   a.o_cont = reinterpret_cast<float*>(ws + L.o_cont);
@@ -1322,7 +1504,8 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
   a.P = P;
   a.window = window;
   a.max_new = max_new;
-  a.prefix_few = P > 0 && rows * a.gq <= FEW;
+  a.few = p.few;
+  a.prefix_few = P > 0 && rows * a.gq <= p.few;
   // key tiles that an item can have: all, or what a window reaches
   auto tiles = [&](long long keys) {
     if (window > 0 && keys > (long long)window + max_new + 128) keys = (long long)window + max_new + 128;
@@ -1330,6 +1513,8 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
   };
   a.ns_prefix = P == 0 ? 0 : (a.prefix_few ? 1 : pieces_for(p.prefix_items, tiles(P), sms, p.prefix_cap));
   a.ns_own = p.many ? pieces_for(p.own_items, tiles((long long)width * page), sms, p.own_cap) : 1;
+  // one own piece a row, and little of the prefix's to read back: join in the epilogue
+  a.own_joins = p.many && a.ns_own == 1 && a.ns_prefix <= 4;
   a.G = p.G;
   a.scale_log2 = float(1.4426950408889634 / sqrt(double(hd)));
   return hd == 64 ? launch_shared<64>(a, k, v, p, sms, st) : launch_shared<128>(a, k, v, p, sms, st);

@@ -38,6 +38,7 @@ __host__ __device__ constexpr int wsp_bytes(int nb) { return NW * 2 * 32 * 4 * n
 constexpr int MAX_B = 16;
 constexpr int MAX_LAYERS = 128;
 constexpr int MAX_PAGED_BATCH = 4096;  // sequences of one call on the paged cache
+constexpr int MAX_PAGED_KV = 64;       // KV heads
 constexpr int MAX_PAGED_GQ = 16;       // query heads per KV head on the paged cache
 constexpr int MAX_GQ = 8;              // query heads per KV head supported by the attention tile
 // A GEMV phase whose K is split into more than RED_NS slabs (batch > 1) sums

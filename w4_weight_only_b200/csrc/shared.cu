@@ -161,7 +161,7 @@ struct Tc {
   static constexpr int TILE = 128 * HD * 2;                 // 128 rows, bytes
   static constexpr int PANEL = 128 * 128;
   static constexpr int NQ = ALT ? 1 : 2;
-  static constexpr int NS = HD == 128 ? (ALT ? 3 : 4) : (ALT ? 6 : 8);  // K / V ring slots
+  static constexpr int NS = HD == 128 ? (ALT ? 5 : 4) : 8;  // K / V ring slots
   static constexpr int ROWS = NQ * 128;
   static constexpr int BARS = 512;
   static constexpr int SMEM = (NQ + NS) * TILE + BARS + 1024;
@@ -173,7 +173,7 @@ struct Tc {
 constexpr int TC_THREADS = 320;
 
 template <int HD, bool ALT>
-__global__ void __launch_bounds__(TC_THREADS, 1) __maxnreg__(ALT ? 128 : 168)
+__global__ void __launch_bounds__(TC_THREADS, 1)
     tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ ShArgs a, const int own, const int lead) {
   using C = Tc<HD, ALT>;
@@ -523,82 +523,71 @@ __global__ void __launch_bounds__(TC_THREADS, 1) __maxnreg__(ALT ? 128 : 168)
         }
         const int ilo = vlo - kb, ihi = vhi - kb;  // visible: ilo <= i < ihi
         const bool part = __any_sync(0xffffffffu, live && (ilo > 0 || ihi < 128));
-        auto hide = [&](uint32_t (&v)[32], int c0) {
+        uint32_t v[4][32];
+        uint64_t sum_a = 0, sum_b = 0;
+        uint64_t scale2 = 0, nref2 = 0;
+        if (warp_live) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(tS + uint32_t(32 * c), v[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_wait32(v[c]);
           if (part) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (c0 + i < ilo || c0 + i >= ihi) v[i] = 0xff800000u;  // -inf
+            for (int i = 0; i < 128; ++i)
+              if (i < ilo || i >= ihi) v[i >> 5][i & 31] = 0xff800000u;  // -inf
           }
-        };
-        uint32_t v0[32], v1[32];
-        float mx = -INFINITY;
-        if (warp_live) {
-          auto top = [&](uint32_t (&v)[32], int c0) {
-            hide(v, c0);
-            float m0 = mx, m1 = __uint_as_float(v[1]);
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              m0 = fmaxf(fmaxf(m0, __uint_as_float(v[i])), __uint_as_float(v[i + 2]));
-              m1 = fmaxf(fmaxf(m1, __uint_as_float(v[i + 1])), __uint_as_float(v[i + 3]));
-            }
-            mx = fmaxf(m0, m1);
-          };
-          tmem_ld32(tS, v0);
+          for (int i = 0; i < 32; i += 2)
 #pragma unroll
-          for (int c = 0; c < 128; c += 64) {
-            tmem_ld_wait32(v0);
-            tmem_ld32(tS + uint32_t(c + 32), v1);
-            top(v0, c);
-            tmem_ld_wait32(v1);
-            tmem_ld32(tS + uint32_t(c == 0 ? 64 : 0), v0);  // last: the first columns again, for the weights
-            top(v1, c + 32);
-          }
-          mx *= a.scale_log2;
-          float alpha = 1.f;
-          if (mx > m_run + RESCALE) {  // also the first finite maximum of the row
-            alpha = exp2f(m_run - mx);  // 0 while the reference was -inf
-            m_run = mx;
-          }
-          l_run *= alpha;
-          // O rows whose reference moved (the group's previous P V has completed: S_i's barrier follows it)
-          if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-            tmem_ld_wait32(v0);
+            for (int c = 0; c < 4; ++c)
+              mx[c] = fmaxf(fmaxf(mx[c], __uint_as_float(v[c][i])), __uint_as_float(v[c][i + 1]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+          if (__any_sync(0xffffffffu, top > m_run + RESCALE)) {  // also the first finite maximum of a row
+            const bool up = top > m_run + RESCALE;
+            const float alpha = up ? exp2f(m_run - top) : 1.f;  // 0 while the reference was -inf
+            if (up) m_run = top;
+            l_run *= alpha;
+            // the group's previous P V has completed: S_i's barrier follows it
+            if (j > 0) {
 #pragma unroll 1
-            for (int c = 0; c < HD; c += 32) {
-              tmem_ld32(tO + uint32_t(c), v1);
-              tmem_ld_wait32(v1);
+              for (int c = 0; c < HD; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + uint32_t(c), o);
+                tmem_ld_wait();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v1[i] = __float_as_uint(__uint_as_float(v1[i]) * alpha);
-              tmem_st32(tO + uint32_t(c), v1);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                tmem_st16(tO + uint32_t(c), o);
+              }
             }
           }
+          const float nref = m_run == -INFINITY ? 0.f : -m_run;
+          scale2 = pack_f32x2(a.scale_log2, a.scale_log2);
+          nref2 = pack_f32x2(nref, nref);
         }
-        const float nref = m_run == -INFINITY ? 0.f : -m_run;
-        const uint64_t scale2 = pack_f32x2(a.scale_log2, a.scale_log2), nref2 = pack_f32x2(nref, nref);
-        uint64_t sum2 = 0;
-        auto weights = [&](uint32_t (&v)[32], int c0) {
-          hide(v, c0);
+        auto weights = [&](uint32_t (&w)[32], int c) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2) {
-            const uint64_t x =
-                fma_f32x2(pack_f32x2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), scale2, nref2);
-            float x0, x1;
-            unpack_f32x2(x, x0, x1);
-            const float p0 = ex2_fast(x0), p1 = ex2_fast(x1);
-            sum2 = add_f32x2(sum2, pack_f32x2(p0, p1));
-            v[i >> 1] = cvt_bf16x2(p0, p1);
+          for (int i = 0; i < 32; i += 4) {
+            const uint64_t xa =
+                fma_f32x2(pack_f32x2(__uint_as_float(w[i]), __uint_as_float(w[i + 1])), scale2, nref2);
+            const uint64_t xb =
+                fma_f32x2(pack_f32x2(__uint_as_float(w[i + 2]), __uint_as_float(w[i + 3])), scale2, nref2);
+            float x0, x1, x2, x3;
+            unpack_f32x2(xa, x0, x1);
+            unpack_f32x2(xb, x2, x3);
+            const float p0 = ex2_fast(x0), p1 = ex2_fast(x1), p2 = ex2_fast(x2), p3 = ex2_fast(x3);
+            sum_a = add_f32x2(sum_a, pack_f32x2(p0, p1));
+            sum_b = add_f32x2(sum_b, pack_f32x2(p2, p3));
+            w[i >> 1] = cvt_bf16x2(p0, p1);
+            w[(i >> 1) + 1] = cvt_bf16x2(p2, p3);
           }
-          tmem_st16(tP + uint32_t(c0 >> 1), v);
+          tmem_st16(tP + uint32_t(16 * c), w);
         };
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (warp_live) {
-            tmem_ld_wait32(v0);
-            tmem_ld32(tS + uint32_t(half * 64 + 32), v1);
-            weights(v0, half * 64);
-            tmem_ld_wait32(v1);
-            if (half == 0) tmem_ld32(tS + 64u, v0);
-            weights(v1, half * 64 + 32);
+            weights(v[2 * half], 2 * half);
+            weights(v[2 * half + 1], 2 * half + 1);
             tmem_st_wait();
           }
           tc_fence_before();
@@ -606,7 +595,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1) __maxnreg__(ALT ? 128 : 168)
           if (lane == 0) mbar_arrive(p_full + grp * 2 + half);
         }
         float s0, s1;
-        unpack_f32x2(sum2, s0, s1);
+        unpack_f32x2(add_f32x2(sum_a, sum_b), s0, s1);
         l_run += s0 + s1;
       }
     }

@@ -53,6 +53,7 @@ struct ShArgs {
   float2* ml_cont;      // [G][few]
   int rows, batch, nq, nkv, gq, n_pages, page_log2, width, P, window, max_new;
   int ns_prefix;        // pieces of the prefix (slots 0 ..), 0 without one
+  int ns_rest;          // of them, for the rows behind the last whole pair tile
   int ns_own;           // pieces of the own positions in tc_kernel (slots ns_prefix ..)
   int few;              // packed rows of a sequence that few_kernel takes (16, 32 or 48)
   int prefix_few;       // 1: few_kernel takes the prefix too (few packed rows in all)
@@ -145,7 +146,8 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
 // softmax:
 //  PAIR: two tiles of 128 rows, group i has tile i, both use every K / V tile.
 //  ALT (at most 128 rows): one tile of rows, group i has the key tiles of
-//        parity i, and the groups' pieces are joined at the end.
+//        parity i, and the groups' pieces are joined at the end.  A key tile
+//        takes half of PAIR's time.
 // S_i = Q K^T into TMEM columns [128 i, + 128); the group reads its rows twice
 // (32 columns at a time: the maximum, then the weights; a second read of TMEM
 // costs less than 128 registers and four times the code), forms P = 2^(s - m)
@@ -156,36 +158,34 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
 // maximum has risen by more than 2^8 over it, so O is rescaled rarely; P <=
 // 2^8 is rounded to bf16, 2^-8 of each weight at most, while l sums the
 // weights unrounded in fp32.
-template <int HD, bool ALT>
+template <int HD>
 struct Tc {
   static constexpr int TILE = 128 * HD * 2;                 // 128 rows, bytes
   static constexpr int PANEL = 128 * 128;
-  static constexpr int NQ = ALT ? 1 : 2;
-  static constexpr int NS = HD == 128 ? (ALT ? 5 : 4) : 8;  // K / V ring slots
-  static constexpr int ROWS = NQ * 128;
+  static constexpr int NT = HD == 128 ? 6 : 10;             // tiles in shared memory: Q (ALT 1, PAIR 2), the others the K / V ring
   static constexpr int BARS = 512;
-  static constexpr int SMEM = (NQ + NS) * TILE + BARS + 1024;
+  static constexpr int SMEM = NT * TILE + BARS + 1024;
   static constexpr int O_COL = 256;                         // O_i at 256 + i HD
   static constexpr int P_COL(int i) { return HD == 128 ? i * 128 : 384 + i * 64; }
   static constexpr int LD = HD + 4;                         // floats between the rows of O in shared memory
-  static_assert(NQ * 128 * (LD * 4 + 16) <= (NQ + NS) * TILE, "O tiles fit where Q, K and V were");
+  static_assert(256 * (LD * 4 + 16) <= NT * TILE, "O tiles fit where Q, K and V were");
 };
 constexpr int TC_THREADS = 320;
+constexpr int TC_ROWS = 256;  // packed rows of a tile pair
 
-template <int HD, bool ALT>
+template <int HD>
 __global__ void __launch_bounds__(TC_THREADS, 1)
     tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
               const __grid_constant__ ShArgs a, const int own, const int lead) {
-  using C = Tc<HD, ALT>;
-  constexpr int NS = C::NS, TILE = C::TILE, PANEL = C::PANEL, LD = C::LD;
+  using C = Tc<HD>;
+  constexpr int TILE = C::TILE, PANEL = C::PANEL, LD = C::LD;
   extern __shared__ uint8_t tc_raw[];
   uint8_t* sm = tc_raw + ((1024u - (smem_addr(tc_raw) & 1023u)) & 1023u);
   uint8_t* sQ = sm;
-  uint8_t* sR = sm + C::NQ * TILE;
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(sR + NS * TILE);
-  uint64_t* kv_full = q_full + 1;        // [NS]
-  uint64_t* kv_empty = kv_full + NS;     // [NS]
-  uint64_t* s_full = kv_empty + NS;      // [2]: S_i computed (and every earlier MMA done)
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(sm + C::NT * TILE);
+  uint64_t* kv_full = q_full + 1;        // [NT]
+  uint64_t* kv_empty = kv_full + C::NT;  // [NT]
+  uint64_t* s_full = kv_empty + C::NT;     // [2]: S_i computed (and every earlier MMA done)
   uint64_t* p_full = s_full + 2;         // [2][2]: half of P_i written, O_i rescaled (4 warps arrive)
   uint64_t* o_done = p_full + 4;
   uint32_t* tbase = reinterpret_cast<uint32_t*>(o_done + 1);
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   if (tid == 0) {
     mbar_init(q_full, 8);
 #pragma unroll 1
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < C::NT; ++s) {
       mbar_init(kv_full + s, 1);
       mbar_init(kv_empty + s, 1);
     }
@@ -224,16 +224,24 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   // tokens r0 .., piece of the keys ----
   int kvh, piece, ns, base, valid, r0, b = 0, n = 0, len = 0;
   if (!own) {
-    const int packed = total_rows(a) * a.gq;
-    const int ntile = (a.rows * a.gq + C::ROWS - 1) / C::ROWS;
+    // whole pair tiles in ns_prefix pieces each, then the rest of the rows: a
+    // rest of at most 128 rows takes half the time a key, in ns_rest pieces
+    const int packed = total_rows(a) * a.gq, whole = a.rows * a.gq / TC_ROWS;
     int x = blockIdx.x;
-    base = (x % ntile) * C::ROWS;
-    x /= ntile;
+    const int heads = whole * a.nkv;
+    r0 = 0;
+    if (x < heads * a.ns_prefix) {
+      ns = a.ns_prefix;
+      base = (x % whole) * TC_ROWS;
+      x /= whole;
+    } else {
+      x -= heads * a.ns_prefix;
+      ns = a.ns_rest;
+      base = whole * TC_ROWS;
+    }
     kvh = x % a.nkv;
     piece = x / a.nkv;
-    ns = a.ns_prefix;
-    r0 = 0;
-    valid = min(C::ROWS, packed - base);
+    valid = min(TC_ROWS, packed - base);
   } else {
     int x = blockIdx.x;
     ns = a.ns_own;
@@ -247,7 +255,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       int t = 0;
       if (tid < 256 && c0 + tid < a.batch) {
         const Seq s = load_seq(a, c0 + tid);
-        if (s.n * a.gq > a.few) t = (s.n * a.gq + C::ROWS - 1) / C::ROWS;
+        if (s.n * a.gq > a.few) t = (s.n * a.gq + TC_ROWS - 1) / TC_ROWS;
       }
       int incl = t;
 #pragma unroll
@@ -280,26 +288,29 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       n = s.n;
       len = s.len;
       r0 = s.r0;
-      const int nt = (n * a.gq + C::ROWS - 1) / C::ROWS;
-      base = (nt - 1 - (want - s_b[1])) * C::ROWS;  // the longest rows first
-      valid = min(C::ROWS, n * a.gq - base);
+      const int nt = (n * a.gq + TC_ROWS - 1) / TC_ROWS;
+      base = (nt - 1 - (want - s_b[1])) * TC_ROWS;  // the longest rows first
+      valid = min(TC_ROWS, n * a.gq - base);
     }
   }
 
   // ---- this thread's row: token, head, its query; the visible keys [vlo,
   // vhi) (prefix positions, or own positions) ----
+  const bool alt = valid <= 128;
+  const int NS = C::NT - (alt ? 1 : 2);  // ring slots
+  uint8_t* sR = sm + (alt ? 1 : 2) * TILE;
   const int grp = (warp >> 2) & 1, r = (warp & 3) * 32 + lane;
-  const int prow = base + (ALT ? 0 : grp * 128) + r;
+  const int prow = base + (alt ? 0 : grp * 128) + r;
   const bool live = warp < 8 && prow < base + valid;
   const int row_tok = live ? prow / a.gq : 0;
   const int tok = r0 + row_tok, head = kvh * a.gq + (live ? prow - row_tok * a.gq : 0);
-  constexpr int CH = HD / 8, QN = ALT ? CH / 2 : CH;  // 16-byte chunks of a row; of it that this thread brings
-  const int qc0 = ALT ? grp * QN : 0;
-  uint4 qv[QN];
+  constexpr int CH = HD / 8;  // 16-byte chunks of a row (ALT: each group brings half of them)
+  uint4 qv[CH];
   if (live) {
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)tok * a.nq + head) * HD) + qc0;
+    const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)tok * a.nq + head) * HD);
 #pragma unroll
-    for (int c = 0; c < QN; ++c) qv[c] = src[c];
+    for (int c = 0; c < CH; ++c)
+      if (!alt || (c < CH / 2) == (grp == 0)) qv[c] = src[c];
   }
   int vlo = 0, vhi = 0, k_lo = 0, k_hi = a.P;  // k: keys that some row of the item sees
   if (own) {
@@ -342,19 +353,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     t0 = f + int((long long)nt * piece / ns);
     nb = f + int((long long)nt * (piece + 1) / ns) - t0;
   }
-  const int groups = valid <= 0 ? 0 : ((ALT ? nb > 1 : valid > 128) ? 2 : 1);
+  const int groups = valid <= 0 ? 0 : ((alt ? nb > 1 : true) ? 2 : 1);
   const int32_t* pages = own ? a.table + (size_t)b * a.width : a.ptable;
 
   if (warp == 8) {
     // ---- loads, in the order in which the MMAs use them: K_0 (K_1) V_0 K_2 V_1 .. (ALT), K_0 V_0 K_1 V_1 .. (PAIR)
-    uint32_t it = 0;
+    int s = 0, lap = 0;
     bool ok = true;
     auto put = [&](const CUtensorMap* map, int t) {
       if (!ok) return;
-      const int s = int(it % NS);
-      if (it >= uint32_t(NS)) {
+      if (lap > 0) {
         int good = 1;
-        if (lane == 0) good = sh_wait(kv_empty + s, ((it / NS) - 1u) & 1u, abort_flag, a.err) ? 1 : 0;
+        if (lane == 0) good = sh_wait(kv_empty + s, uint32_t(lap - 1) & 1u, abort_flag, a.err) ? 1 : 0;
         if (!__shfl_sync(0xffffffffu, good, 0)) {
           ok = false;
           return;
@@ -365,9 +375,12 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       if (lane == 0) mbar_expect_tx(kv_full + s, load_blocks<128>(kb, k_hi, a.page_log2) * bs * HD * 2);
       __syncwarp();
       load_tile<HD, 128>(sR + s * TILE, map, pages, kb, k_hi, kvh, kv_full + s, a, lane);
-      ++it;
+      if (++s == NS) {
+        s = 0;
+        ++lap;
+      }
     };
-    if (ALT) {
+    if (alt) {
       if (nb > 0) put(&tmK, 0);
       if (nb > 1) put(&tmK, 1);
 #pragma unroll 1
@@ -383,33 +396,43 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
     }
     if (lane == 0) {
-      const uint32_t first = it > uint32_t(NS) ? it - NS : 0u;
-#pragma unroll 1
-      for (uint32_t j = first; j < it; ++j) sh_drain(kv_full + (j % NS), (j / NS) & 1u, a.err);
+      // each slot's last load
+      for (int i = 0; i < NS; ++i) {
+        const int laps = lap + (i < s ? 1 : 0);
+        if (laps > 0) sh_drain(kv_full + i, uint32_t(laps - 1) & 1u, a.err);
+      }
     }
   } else if (warp == 9) {
     // ---- MMAs (one thread) ----
     if (lane == 0 && nb > 0) {
       const uint32_t idS = umma_idesc_f16(128, 128, true);
       const uint32_t idO = umma_idesc_f16(128, HD, true) | UMMA_B_MN;
-      auto ready = [&](uint32_t i) {
-        const bool w = sh_wait(kv_full + i % NS, (i / NS) & 1u, abort_flag, a.err);
+      // descriptors of the first tiles; a byte offset adds its sixteenth to the start address
+      const uint64_t dQ = umma_desc_sw128(sQ, 0), dK = umma_desc_sw128(sR, 0), dV = umma_desc_mn_sw128(sR, PANEL, 1024);
+      int s = 0;          // the next ring slot to take
+      uint32_t lap = 0;
+      auto take = [&](int& slot) {
+        slot = s;
+        const bool w = sh_wait(kv_full + s, lap & 1u, abort_flag, a.err);
         tc_fence_after();
+        if (++s == NS) {
+          s = 0;
+          ++lap;
+        }
         return w;
       };
-      auto issue_s = [&](int qi, uint32_t ki) {
-        const uint8_t* q = sQ + (ALT ? 0 : qi) * TILE;
-        const uint8_t* k = sR + (ki % NS) * TILE;
+      auto issue_s = [&](int qi, int ki) {
+        const uint64_t q = dQ + uint32_t((alt ? 0 : qi) * (TILE >> 4)), k = dK + uint32_t(ki * (TILE >> 4));
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
-          const uint32_t off = uint32_t((ks >> 2) * PANEL + (ks & 3) * 32);
-          umma_f16(tmem + uint32_t(qi * 128), umma_desc_sw128(q, off), umma_desc_sw128(k, off), idS, ks > 0 ? 1u : 0u);
+          const uint32_t off = uint32_t((ks >> 2) * PANEL + (ks & 3) * 32) >> 4;
+          umma_f16(tmem + uint32_t(qi * 128), q + off, k + off, idS, ks > 0 ? 1u : 0u);
         }
         umma_commit(s_full + qi);
       };
       // O_qi (+)= P_qi V: each half of the keys when its weights are there
-      auto issue_pv = [&](int qi, uint32_t vi, int j) {
-        const uint8_t* v = sR + (vi % NS) * TILE;
+      auto issue_pv = [&](int qi, int vi, int j) {
+        const uint64_t v = dV + uint32_t(vi * (TILE >> 4));
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!sh_wait(p_full + qi * 2 + half, uint32_t(j) & 1u, abort_flag, a.err)) return false;
@@ -418,56 +441,49 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           for (int k4 = 0; k4 < 4; ++k4) {
             const int ks = half * 4 + k4;
             umma_f16_ts(tmem + uint32_t(C::O_COL + qi * HD), tmem + uint32_t(C::P_COL(qi) + ks * 8),
-                        umma_desc_mn_sw128(v + ks * 16 * 128, PANEL, 1024), idO, (j == 0 && ks == 0) ? 0u : 1u);
+                        v + uint32_t(ks * 16 * 128 >> 4), idO, (j == 0 && ks == 0) ? 0u : 1u);
           }
         }
         return true;
       };
       bool ok = sh_wait(q_full, 0u, abort_flag, a.err);
-      uint32_t it = 0;
-      if (ALT) {
+      int ks = 0, vs = 0;  // slots of the K and V tiles in use
+      if (alt) {
         for (int t = 0; t < 2 && t < nb && ok; ++t) {
-          ok = ready(it);
-          if (!ok) break;
-          issue_s(t, it);
-          umma_commit(kv_empty + it % NS);
-          ++it;
+          if (!(ok = take(ks))) break;
+          issue_s(t, ks);
+          umma_commit(kv_empty + ks);
         }
 #pragma unroll 1
         for (int t = 0; t < nb && ok; ++t) {
-          if (!(ok = ready(it) && issue_pv(t & 1, it, t >> 1))) break;
-          umma_commit(kv_empty + it % NS);
-          ++it;
+          if (!(ok = take(vs) && issue_pv(t & 1, vs, t >> 1))) break;
+          umma_commit(kv_empty + vs);
           if (t + 2 < nb) {
-            if (!(ok = ready(it))) break;
-            issue_s(t & 1, it);
-            umma_commit(kv_empty + it % NS);
-            ++it;
+            if (!(ok = take(ks))) break;
+            issue_s(t & 1, ks);
+            umma_commit(kv_empty + ks);
           }
         }
       } else {
-        if (ok && (ok = ready(0))) {
-          issue_s(0, 0);
-          if (groups == 2) issue_s(1, 0);
-          umma_commit(kv_empty + 0);
+        if (ok && (ok = take(ks))) {
+          issue_s(0, ks);
+          issue_s(1, ks);
+          umma_commit(kv_empty + ks);
         }
 #pragma unroll 1
         for (int j = 0; j < nb && ok; ++j) {
-          const uint32_t vt = 2u * j + 1u, kn = 2u * j + 2u;
           const bool more = j + 1 < nb;
-          if (!(ok = ready(vt) && issue_pv(0, vt, j))) break;
+          if (!(ok = take(vs) && issue_pv(0, vs, j))) break;
           if (more) {
-            if (!(ok = ready(kn))) break;
-            issue_s(0, kn);
+            if (!(ok = take(ks))) break;
+            issue_s(0, ks);
           }
-          if (groups == 2) {
-            if (!(ok = issue_pv(1, vt, j))) break;
-            umma_commit(kv_empty + vt % NS);
-            if (more) issue_s(1, kn);
-          } else {
-            umma_commit(kv_empty + vt % NS);
+          if (!(ok = issue_pv(1, vs, j))) break;
+          umma_commit(kv_empty + vs);
+          if (more) {
+            issue_s(1, ks);
+            umma_commit(kv_empty + ks);
           }
-          if (more) umma_commit(kv_empty + kn % NS);
         }
       }
       umma_commit(o_done);
@@ -477,12 +493,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   } else {
     // ---- the rows of Q into shared memory (128-byte swizzle; ALT: half of each row per group) ----
     if (live) {
-      uint8_t* dst = sQ + (ALT ? 0 : grp) * TILE + r * 128;
+      uint8_t* dst = sQ + (alt ? 0 : grp) * TILE + r * 128;
 #pragma unroll
-      for (int k = 0; k < QN; ++k) {
-        const int c = qc0 + k;
-        *reinterpret_cast<uint4*>(dst + (c >> 3) * PANEL + (((c & 7) ^ (r & 7)) << 4)) = qv[k];
-      }
+      for (int c = 0; c < CH; ++c)
+        if (!alt || (c < CH / 2) == (grp == 0))
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * PANEL + (((c & 7) ^ (r & 7)) << 4)) = qv[c];
     }
     fence_proxy_async();
     __syncwarp();
@@ -497,18 +512,18 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     int j = 0;
     if (grp < groups) {
 #pragma unroll 1
-      for (int t = ALT ? grp : 0; t < nb; t += ALT ? 2 : 1, ++j) {
+      for (int t = alt ? grp : 0; t < nb; t += alt ? 2 : 1, ++j) {
         const int kb = (t0 + t) * 128;
         // keys that no row sees: their values must be finite (0 x NaN), so
         // group 0 (ALT: the tile's group) clears those rows of V
-        const bool edge = (kb < k_lo || kb + 128 > k_hi) && (ALT || grp == 0);
+        const bool edge = (kb < k_lo || kb + 128 > k_hi) && (alt || grp == 0);
         if (!__all_sync(0xffffffffu, sh_wait(s_full + grp, uint32_t(j) & 1u, abort_flag, a.err))) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (edge) {
-          const uint32_t vi = ALT ? uint32_t(t == nb - 1 ? 2 * nb - 1 : 2 * t + 2) : 2u * t + 1u;
+          const uint32_t vi = alt ? uint32_t(t == nb - 1 ? 2 * nb - 1 : 2 * t + 2) : 2u * t + 1u;
           if (!__all_sync(0xffffffffu, sh_wait(kv_full + vi % NS, (vi / NS) & 1u, abort_flag, a.err))) {
             ok = false;
             break;
@@ -565,6 +580,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           scale2 = pack_f32x2(a.scale_log2, a.scale_log2);
           nref2 = pack_f32x2(nref, nref);
         }
+        // weights of 32 keys.  (Part of them by a polynomial on the FMA pipe, to
+        // relieve the special-function unit, was slower at every share: 728 us
+        // without, 741 at an eighth, 756 at a quarter, 816 at a half of them,
+        // for a prompt of 8,192.)
         auto weights = [&](uint32_t (&w)[32], int c) {
 #pragma unroll
           for (int i = 0; i < 32; i += 4) {
@@ -603,9 +622,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     // written whole; (m, l) of each row beside them ----
     ok = ok && (nb == 0 || __all_sync(0xffffffffu, sh_wait(o_done, 0u, abort_flag, a.err)));
     tc_fence_after();
-    const bool join = ALT && groups == 2;
-    float* sO = reinterpret_cast<float*>(sm) + (ALT ? 0 : grp * 128 * LD);  // [128][LD]
-    float4* s_row = reinterpret_cast<float4*>(sm + C::NQ * 128 * LD * 4) + (ALT ? 0 : grp * 128);
+    const bool join = alt && groups == 2;
+    float* sO = reinterpret_cast<float*>(sm) + (alt ? 0 : grp * 128 * LD);  // [128][LD]
+    float4* s_row = reinterpret_cast<float4*>(sm + 256 * LD * 4) + (alt ? 0 : grp * 128);
     float* mine = sO + r * LD;
     auto dump = [&](float f, bool add, float g) {
 #pragma unroll 1
@@ -633,7 +652,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       asm volatile("bar.sync 1, 256;" ::: "memory");
     }
-    if (grp < (ALT ? min(groups, 1) : groups) && warp_live && ok) {
+    if (grp < (alt ? min(groups, 1) : groups) && warp_live && ok) {
       float f0 = 1.f, f1 = 0.f;
       if (join) {
         const float4 o = s_row[r];
@@ -645,7 +664,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       }
       const bool final = own && a.own_joins;
       const size_t stride = (size_t)a.rows * a.nq;
-      const int np = final ? a.ns_prefix : 0;
+      const int np = final ? a.ns_prefix : 0;  // (with own_joins every row has as many)
       if (np > 0) wait_previous_kernel();  // the prefix's pieces, made by the launch before this one
       if (final) {
         // the weights of this piece and of the prefix's in the joined row
@@ -673,7 +692,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       s_row[r] = make_float4(m_run, l_run, __int_as_float(tok * a.nq + head), 0.f);
       __syncwarp();
       // a warp writes its 32 rows, one after the other, 16 bytes a lane
-      const int w0 = (warp & 3) * 32, rows = min(32, valid - (ALT ? 0 : grp * 128) - w0);
+      const int w0 = (warp & 3) * 32, rows = min(32, valid - (alt ? 0 : grp * 128) - w0);
       const int part = own ? a.ns_prefix + piece : piece;
       constexpr int LPR = HD / 4;  // lanes of a row
       const int sub = lane / LPR, col = (lane % LPR) * 4;
@@ -742,8 +761,8 @@ struct Fw {
   static constexpr int ROWS = 16 * MG;
   static constexpr int NW = 4 * MG;                // math warps
   static constexpr int THREADS = 32 * (NW + 1);
-  static constexpr int PER_SM = MG == 1 ? 3 : 1;   // CTAs that are resident together
-  static constexpr int NST = (MG == 1 ? 2 : 5) * (HD == 128 ? 1 : 2);  // stages
+  static constexpr int PER_SM = 4 - MG;            // CTAs that are resident together
+  static constexpr int NST = (MG == 1 ? 2 : (MG == 2 ? 3 : 5)) * (HD == 128 ? 1 : 2);  // stages
   static constexpr bool LO = MG == 1;
   static constexpr int QB = ROWS * HD * 2;
   static constexpr int SMEM = NST * 2 * KV + QB + 1024;
@@ -806,11 +825,10 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
   extern __shared__ uint8_t fw_raw[];
   uint8_t* sm = fw_raw + ((1024u - (smem_addr(fw_raw) & 1023u)) & 1023u);
   uint8_t* sQ = sm + NST * 2 * KV;
-  int* cum = reinterpret_cast<int*>(sQ + C::QB);  // [batch + 2]
   __shared__ uint64_t full[NST], empty[NST];
   __shared__ float2 s_ml[4][16];
   __shared__ int s_vlo[ROWS], s_vhi[ROWS];
-  __shared__ int s_warp[C::NW + 1], s_lo, s_bad, s_abort;
+  __shared__ int s_abort;
   volatile int* abort_flag = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -820,60 +838,55 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
     }
     fence_mbar_init();
     s_abort = 0;
-    s_lo = 0x7fffffff;
-    s_bad = 0;
-    cum[0] = 0;
   }
+  __syncthreads();
   if (lead) wait_previous_kernel();  // as in tc_kernel
   launch_dependents();
-  // ---- the stream: tiles before each sequence ----
-  int before = 0;
-#pragma unroll 1
-  for (int c0 = 0; c0 < a.batch; c0 += C::THREADS) {
-    int t = 0;
-    Seq s{0, 0, 0, 1};
-    if (c0 + tid < a.batch) {
-      s = load_seq(a, c0 + tid);
-      int lo;
-      t = few_tiles(a, s, &lo);
-    }
-    int incl = t;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += u;
-    }
-    __syncthreads();  // the initial values; the last round's s_warp has been read
-    if (!s.ok) s_bad = 1;
-    if (a.prefix_few && s.n > 0) atomicMin(&s_lo, a.P + s.len - s.n);
-    if (lane == 31) s_warp[warp] = incl;
-    __syncthreads();
-    int off = before;
-#pragma unroll
-    for (int w = 0; w < C::NW + 1; ++w) {
-      if (w < warp) off += s_warp[w];
-      before += s_warp[w];
-    }
-    if (c0 + tid < a.batch) cum[c0 + tid + 1] = off + incl;
-  }
-  const int p_lo = few_prefix_lo(a, s_lo);
-  before += few_prefix_tiles(a, s_lo);
-  if (tid == 0) cum[a.batch + 1] = before;
-  __syncthreads();
-  if (blockIdx.x == 0 && tid == 0 && s_bad) sh_error(a.err, EW_BAD_SHAPE);
-  const Runs runs(before * a.nkv, a.G);
+  // ---- the stream and this CTA's run of it: each warp by itself, a sequence
+  // a lane (the first 32 stay in registers) ----
+  auto tiles_of = [&](int b, int& bad, int& first_pos) {
+    if (b >= a.batch) return 0;
+    const Seq s = load_seq(a, b);
+    int lo;
+    bad |= !s.ok;
+    if (a.prefix_few && s.n > 0) first_pos = min(first_pos, a.P + s.len - s.n);
+    return few_tiles(a, s, &lo);
+  };
+  int bad = 0, first_pos = 0x7fffffff;
+  const int t_first = tiles_of(lane, bad, first_pos);
+  int own_tiles = t_first;
+#pragma unroll 4
+  for (int b = lane + 32; b < a.batch; b += 32) own_tiles += tiles_of(b, bad, first_pos);
+  own_tiles = __reduce_add_sync(0xffffffffu, own_tiles);
+  if (a.prefix_few) first_pos = __reduce_min_sync(0xffffffffu, first_pos);
+  if (blockIdx.x == 0 && warp == 0 && __any_sync(0xffffffffu, bad) && lane == 0) sh_error(a.err, EW_BAD_SHAPE);
+  const int p_lo = few_prefix_lo(a, first_pos), p_tiles = few_prefix_tiles(a, first_pos);
+  const int W = (own_tiles + p_tiles) * a.nkv;
+  const Runs runs(W, a.G);
   const int cta = int(blockIdx.x);
-  const int x_lo = cta < runs.G ? runs.begin(cta) : 0, x_hi = cta < runs.G ? min(runs.begin(cta + 1), before * a.nkv) : 0;
-  // the sequence of the run's first tile
-  int b0 = 0;
+  const int x_lo = cta < runs.G ? runs.begin(cta) : 0, x_hi = cta < runs.G ? min(runs.begin(cta + 1), W) : 0;
+  // the sequence of the run's first tile, and the tiles before it
+  int b0 = a.batch, base0 = own_tiles;
   {
-    int hi = a.batch + 1;
-    while (hi - b0 > 1) {
-      const int mid = (b0 + hi) >> 1;
-      if (cum[mid] * a.nkv <= x_lo)
-        b0 = mid;
-      else
-        hi = mid;
+    const int y = x_lo / a.nkv;
+    int before = 0;
+#pragma unroll 1
+    for (int c0 = 0; c0 < a.batch; c0 += 32) {
+      int incl = c0 == 0 ? t_first : tiles_of(c0 + lane, bad, first_pos);
+      const int t = incl;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += u;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + incl > y);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        b0 = c0 + l;
+        base0 = before + __shfl_sync(0xffffffffu, incl - t, l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, incl, 31);
     }
   }
   auto seq_at = [&](int b) {
@@ -882,12 +895,12 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
       f.s = Seq{0, total_rows(a), 0, 1};
       f.k_lo = p_lo;
       f.k_end = a.P;
+      f.tiles = p_tiles;
     } else {
       f.s = load_seq(a, b);
-      few_tiles(a, f.s, &f.k_lo);
+      f.tiles = few_tiles(a, f.s, &f.k_lo);
       f.k_end = f.s.len;
     }
-    f.tiles = cum[b + 1] - cum[b];
     return f;
   };
 
@@ -895,12 +908,15 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
     // ---- loads ----
     uint32_t it = 0;
     bool ok = true;
-    int b = b0;
+    int b = b0, base = base0;
 #pragma unroll 1
     for (int x = x_lo; x < x_hi && ok;) {
-      while (x >= cum[b + 1] * a.nkv) ++b;
-      const FewSeq f = seq_at(b);
-      const int y = x - cum[b] * a.nkv, kvh = y / f.tiles, t = y - kvh * f.tiles;
+      FewSeq f = seq_at(b);
+      while (x >= (base + f.tiles) * a.nkv) {
+        base += f.tiles;
+        f = seq_at(++b);
+      }
+      const int y = x - base * a.nkv, kvh = y / f.tiles, t = y - kvh * f.tiles;
       const int nt = min(x_hi - x, f.tiles - t);
       const int32_t* pages = b == a.batch ? a.ptable : a.table + (size_t)b * a.width;
       const int bs = min(1 << a.page_log2, 64);
@@ -940,13 +956,16 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
     const uint32_t q_at = smem_addr(sQ) + (16 * mt + (mi & 1) * 8 + r7) * 128 + (((mi >> 1) ^ r7) << 4);
     const uint32_t ring = smem_addr(sm);
     uint32_t st = 0, phase = 0;
-    int b = b0;
+    int b = b0, base = base0;
     bool ok = true;
 #pragma unroll 1
     for (int x = x_lo; x < x_hi && ok;) {
-      while (x >= cum[b + 1] * a.nkv) ++b;
-      const FewSeq f = seq_at(b);
-      const int y = x - cum[b] * a.nkv, kvh = y / f.tiles, t0 = y - kvh * f.tiles;
+      FewSeq f = seq_at(b);
+      while (x >= (base + f.tiles) * a.nkv) {
+        base += f.tiles;
+        f = seq_at(++b);
+      }
+      const int y = x - base * a.nkv, kvh = y / f.tiles, t0 = y - kvh * f.tiles;
       const int nt = min(x_hi - x, f.tiles - t0);
       const int nrow = f.s.n * a.gq, nmt = (nrow + 15) >> 4;
       // ---- Q into shared memory (128-byte swizzle; zero rows up to whole
@@ -1163,8 +1182,8 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
 // join_kernel: CTA = one head and `tpc` tokens, a warp per token at a time.
 // Where a token's pieces are is worked out before the wait for them (the
 // stream's cut again, from the lengths), while they are still being made;
-// behind the wait there is one round of loads per eight pieces, (m, l) and O
-// together.
+// behind the wait a lane takes a piece's (m, l), then the pieces' O come in
+// rounds of eight.
 // ---------------------------------------------------------------------------
 constexpr int JT = 256, JCH = 8;
 
@@ -1244,6 +1263,10 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
         np = runs.of(px + ptiles - 1) + 1 - p0;
       }
     }
+    // prefix rows behind the last whole pair tile have fewer pieces: the slots from ns_rest to ns_prefix are not theirs
+    const int gap = a.ns_prefix - (tok * a.gq + g >= (a.rows * a.gq & ~(TC_ROWS - 1)) ? a.ns_rest : a.ns_prefix);
+    in_slots -= gap;
+    const int cut = a.ns_prefix - gap;
     const int total = in_slots + nc + np, crow = (tok - s.r0) * a.gq + g, prow = tok * a.gq + g;
     const size_t line = (size_t)tok * a.nq + head;
     if (!waited) wait_previous_kernel();
@@ -1251,40 +1274,54 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
     constexpr int E = HD / 32;
     float acc[E] = {}, L = 0.f, M = -INFINITY;
 #pragma unroll 1
-    for (int i0 = 0; i0 < total; i0 += JCH) {
-      float2 ml[JCH];
-      float x[JCH][E];
+    for (int i0 = 0; i0 < total; i0 += 32) {
+      // a lane's piece: where, and its weight (the address arithmetic of 32
+      // pieces at once: a warp by itself takes ~5 clocks an instruction)
+      const int i = min(i0 + lane, total - 1);
+      const bool slot = i < in_slots, mine = i < in_slots + nc;
+      const size_t at = slot ? (size_t)(first + i + (i >= cut ? gap : 0)) * a.rows * a.nq + line
+                             : (size_t)((mine ? c0 + i - in_slots : p0 + i - in_slots - nc) * a.few + (mine ? crow : prow));
+      const float2 ml = (slot ? a.ml_part : a.ml_cont)[at];
+      const float* src = (slot ? a.o_part : a.o_cont) + at * HD;
+      const bool there = i0 + lane < total && ml.y > 0.f;
+      float m = there ? ml.x : -INFINITY;
 #pragma unroll
-      for (int k = 0; k < JCH; ++k) {
-        const int i = min(i0 + k, total - 1);
-        const bool slot = i < in_slots, mine = i < in_slots + nc;
-        const size_t at = slot ? (size_t)(first + i) * a.rows * a.nq + line
-                               : (size_t)(mine ? c0 + i - in_slots : p0 + i - in_slots - nc) * a.few + (mine ? crow : prow);
-        ml[k] = (slot ? a.ml_part : a.ml_cont)[at];
-        const float* src = (slot ? a.o_part : a.o_cont) + at * HD + lane * E;
-        if (E == 4)
-          *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(src);
-        else
-          *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(src);
-        if (i0 + k >= total) ml[k].y = 0.f;
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (m > M) {
+        const float f = exp2f(M - m);
+        M = m;
+        L *= f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= f;
       }
-      float m = M;
+      const float w = there ? exp2f(ml.x - M) : 0.f;
+      L = fmaf(there ? ml.y : 0.f, w, L);  // this lane's share; summed below
+      const int n32 = min(32, total - i0);
+#pragma unroll 1
+      for (int k0 = 0; k0 < n32; k0 += JCH) {
+        float x[JCH][E];
 #pragma unroll
-      for (int k = 0; k < JCH; ++k) m = ml[k].y > 0.f ? fmaxf(m, ml[k].x) : m;
-      const float f = M == -INFINITY ? 0.f : exp2f(M - m);
-      M = m;
-      L *= f;
+        for (int k = 0; k < JCH; ++k) {
+          // (an index past the last piece is read as that piece, with weight 0)
+          const float* s_k = reinterpret_cast<const float*>(
+              __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k0 + k)) + lane * E;
+          if (E == 4)
+            *reinterpret_cast<float4*>(x[k]) = *reinterpret_cast<const float4*>(s_k);
+          else
+            *reinterpret_cast<float2*>(x[k]) = *reinterpret_cast<const float2*>(s_k);
+        }
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] *= f;
+        for (int k = 0; k < JCH; ++k) {
+          const float f = __shfl_sync(0xffffffffu, w, k0 + k);
+          // an empty piece's O was not written
 #pragma unroll
-      for (int k = 0; k < JCH; ++k) {
-        if (!(ml[k].y > 0.f)) continue;  // an empty piece's O was not written
-        const float w = exp2f(ml[k].x - M);
-        L = fmaf(ml[k].y, w, L);
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = fmaf(x[k][e], w, acc[e]);
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(f != 0.f ? x[k][e] : 0.f, f, acc[e]);
+        }
       }
     }
+    // the lanes' shares of L in a fixed order
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
     const float inv = L > 0.f ? 1.f / L : 0.f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + line * HD + lane * E);
 #pragma unroll
@@ -1326,18 +1363,24 @@ cudaError_t page_map(CUtensorMap* m, const void* base, int hd, int page, int64_t
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Pieces along the keys of `items` equal items of `tiles` 128-key tiles: the
-// count with the shortest time, waves x (tiles of a piece + what a piece costs
-// besides: its start, its rows of O written and read again, ~2 tiles).
-int pieces_for(long long items, int tiles, int sms, int cap) {
+// Pieces along the keys of equal items of `tiles` 128-key tiles: the count with
+// the shortest time, waves x (tiles of a piece + what a piece costs besides:
+// its start, its rows of O written and read again, ~3 tiles).  `pairs` items
+// are cut in ns, `rest` ones in *ns_rest = half of that when they run at twice
+// the speed.
+int pieces_for(long long pairs, long long rest, bool rest_fast, int tiles, int sms, int cap, int* ns_rest) {
   int best = 1;
   double best_t = 1e30;
+  *ns_rest = 1;
   for (int ns = 1; ns <= cap && ns <= (tiles < 1 ? 1 : tiles); ++ns) {
-    const double waves = double((items * ns + sms - 1) / sms);
-    const double t = waves * ((tiles + ns - 1) / ns + 2.0);
+    const int nr = pairs == 0 || !rest_fast ? ns : (ns + 1) / 2;
+    const double speed = pairs == 0 && rest_fast ? 0.5 : 1.0;
+    const double waves = double((pairs * ns + rest * nr + sms - 1) / sms);
+    const double t = waves * (speed * ((tiles + ns - 1) / ns) + 3.0);
     if (t < best_t * 0.999) {
       best_t = t;
       best = ns;
+      *ns_rest = nr;
     }
   }
   return best;
@@ -1346,8 +1389,9 @@ int pieces_for(long long items, int tiles, int sms, int cap) {
 struct ShPlan {
   int few;                // packed rows of a sequence that few_kernel takes
   bool many;              // some sequence may have more
-  bool tc_prefix_alt, tc_own_alt;
-  long long prefix_items, own_items;
+  long long pairs, rest;  // prefix items of whole pair tiles, of the rest of the rows
+  bool rest_alt;
+  long long own_items;
   int prefix_cap, own_cap;
   int G;
 };
@@ -1359,21 +1403,20 @@ ShPlan shared_plan(int rows, int batch, int nq, int nkv, int max_new, int sms) {
   const long long most = (long long)(max_new < rows ? max_new : rows) * gq;  // packed rows of one sequence
   p.few = most <= 16 ? 16 : (most <= 32 ? 32 : MAX_FEW);
   p.many = most > p.few;
-  p.tc_prefix_alt = packed <= 128;
-  p.tc_own_alt = most <= 128;
-  p.prefix_items = nkv * ((packed + (p.tc_prefix_alt ? 127 : 255)) / (p.tc_prefix_alt ? 128 : 256));
+  p.pairs = nkv * (packed / TC_ROWS);
+  p.rest = packed % TC_ROWS ? nkv : 0;
+  p.rest_alt = packed % TC_ROWS <= 128;
   // tiles of the sequences with many rows: at most one partly filled tile each
-  const long long tr = p.tc_own_alt ? 128 : 256;
   long long seqs = packed / (p.few + 1) + 1;
   if (seqs > batch) seqs = batch;
-  p.own_items = nkv * (packed / tr + seqs);
+  p.own_items = nkv * (packed / TC_ROWS + seqs);
   auto cap = [&](long long items) {
     const long long c = (2LL * sms + items - 1) / items;
     return int(c < 1 ? 1 : (c > 64 ? 64 : c));
   };
-  p.prefix_cap = cap(p.prefix_items);
+  p.prefix_cap = cap(p.pairs + p.rest);
   p.own_cap = p.many ? cap(p.own_items) : 1;
-  p.G = (p.few == 16 ? Fw<128, 1>::PER_SM : 1) * sms;  // CTAs that are resident together
+  p.G = (p.few == 16 ? Fw<128, 1>::PER_SM : (p.few == 32 ? Fw<128, 2>::PER_SM : Fw<128, 3>::PER_SM)) * sms;  // CTAs that are resident together
   return p;
 }
 
@@ -1428,12 +1471,9 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
   int lead = 1;  // the call's first launch
   for (int own = 0; own < 2; ++own) {
     if (own ? !p.many : !tc_prefix) continue;
-    const bool alt = own ? p.tc_own_alt : p.tc_prefix_alt;
-    const long long items = (own ? p.own_items : p.prefix_items) * (own ? a.ns_own : a.ns_prefix);
+    const long long items = own ? p.own_items * a.ns_own : p.pairs * a.ns_prefix + p.rest * a.ns_rest;
     void* args[] = {&k128, &v128, &a, &own, &lead};
-    const void* fn = alt ? reinterpret_cast<const void*>(&tc_kernel<HD, true>)
-                         : reinterpret_cast<const void*>(&tc_kernel<HD, false>);
-    e = launch(fn, dim3(unsigned(items)), TC_THREADS, alt ? Tc<HD, true>::SMEM : Tc<HD, false>::SMEM, args, st);
+    e = launch(reinterpret_cast<const void*>(&tc_kernel<HD>), dim3(unsigned(items)), TC_THREADS, Tc<HD>::SMEM, args, st);
     if (e != cudaSuccess) return e;
     lead = 0;
   }
@@ -1447,7 +1487,7 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
                                    : reinterpret_cast<const void*>(&few_kernel<HD, 3>);
     const int smem = p.few == 16 ? F1::SMEM : (p.few == 32 ? F2::SMEM : F3::SMEM);
     const int threads = p.few == 16 ? F1::THREADS : (p.few == 32 ? F2::THREADS : F3::THREADS);
-    e = launch(fn, dim3(unsigned(a.G)), threads, smem + ((a.batch + 2) * 4 + 15) / 16 * 16, args, st);
+    e = launch(fn, dim3(unsigned(a.G)), threads, smem, args, st);
     if (e != cudaSuccess) return e;
   }
   // tokens per CTA of the join: one a warp when few, more where most CTAs may find nothing to do
@@ -1500,10 +1540,13 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
     if (window > 0 && keys > (long long)window + max_new + 128) keys = (long long)window + max_new + 128;
     return int((keys + 127) / 128);
   };
-  a.ns_prefix = P == 0 ? 0 : (a.prefix_few ? 1 : pieces_for(p.prefix_items, tiles(P), sms, p.prefix_cap));
-  a.ns_own = p.many ? pieces_for(p.own_items, tiles((long long)width * page), sms, p.own_cap) : 1;
+  int unused;
+  a.ns_prefix = a.ns_rest = P == 0 ? 0 : 1;
+  if (P > 0 && !a.prefix_few)
+    a.ns_prefix = pieces_for(p.pairs, p.rest, p.rest_alt, tiles(P), sms, p.prefix_cap, &a.ns_rest);
+  a.ns_own = p.many ? pieces_for(p.own_items, 0, false, tiles((long long)width * page), sms, p.own_cap, &unused) : 1;
   // one own piece a row, and little of the prefix's to read back: join in the epilogue
-  a.own_joins = p.many && a.ns_own == 1 && a.ns_prefix <= 4;
+  a.own_joins = p.many && a.ns_own == 1 && a.ns_prefix <= 4 && a.ns_rest == a.ns_prefix;
   a.G = p.G;
   a.scale_log2 = float(1.4426950408889634 / sqrt(double(hd)));
   return hd == 64 ? launch_shared<64>(a, k, v, p, sms, st) : launch_shared<128>(a, k, v, p, sms, st);

@@ -399,7 +399,7 @@ W4A_API int w4a_paged_plan(const int32_t* n_new, const int32_t* lens, const int3
  * slot outside the cache, or a negative position, is skipped and reported by
  * w4a_check.  The angle is formed in fp64, so far positions keep their phase.
  * Of cfg n_heads, n_kv_heads, head_dim, eps and the rotation's fields are
- * used; (n_heads + 2 n_kv_heads) * head_dim <= 51,200.  qkv, q_out, the gains
+ * used; (n_heads + 2 n_kv_heads) * head_dim <= 25,600.  qkv, q_out, the gains
  * and the pages 16-byte aligned.  ws as for w4a_paged_plan. */
 W4A_API int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, int64_t ld, int rows, const float* q_gain,
                       const float* k_gain, const int32_t* pos, const int32_t* slots, uint16_t* q_out,

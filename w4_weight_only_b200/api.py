@@ -501,19 +501,27 @@ def attn_prefill(q: torch.Tensor, k_region: torch.Tensor, v_region: torch.Tensor
 # ---------------------------------------------------------------------------
 # paged KV cache, attention behind a shared prefix
 # ---------------------------------------------------------------------------
-def _together(first: torch.Tensor, **others: Optional[torch.Tensor]) -> torch.cuda.device:
-    """Every tensor on the first one's device, which the call then runs on (on
-    that device's current stream)."""
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name}: expected a tensor on {first.device}, got {t.device}")
-    return torch.cuda.device(first.device)
-
-
-def _shaped(t: torch.Tensor, dtype: torch.dtype, name: str, *shape):
+def _ptr(t: torch.Tensor, dtype: torch.dtype, name: str, shape, dev: torch.device) -> int:
+    """The address of a contiguous tensor of that type, shape (a tuple; None:
+    any size) and device.  A step makes these checks a few hundred times, so
+    the common case is one expression."""
+    if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+        return t.data_ptr()
     _need(t, dtype, name)
     if len(t.shape) != len(shape) or any(s is not None and s != d for s, d in zip(shape, t.shape)):
         raise ValueError(f"{name}: expected shape {list(shape)}, got {list(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name}: expected a tensor on {dev}, got {t.device}")
+    return t.data_ptr()
+
+
+def _call_on(dev: torch.device, name: str, *args):
+    """call() on a device and its current stream (the last argument)."""
+    if dev.index == torch.cuda.current_device():
+        call(name, *args, torch._C._cuda_getCurrentRawStream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            call(name, *args, torch._C._cuda_getCurrentRawStream(dev.index))
 
 
 class PagedKVCache:
@@ -563,26 +571,21 @@ def paged_plan(n_new: torch.Tensor, lens: torch.Tensor, state: torch.Tensor, que
     the free queue [n_pages] with its state {head, count}; queue and table
     [B, width] are updated in place.  check(ws) raises if pages, table width or
     rows did not suffice (nothing has changed then)."""
-    B = n_new.numel()
-    _shaped(n_new, torch.int32, "n_new", None)
-    _shaped(lens, torch.int32, "lens", B)
-    _shaped(state, torch.int32, "state", 2)
-    _shaped(queue, torch.int32, "queue", None)
-    _shaped(table, torch.int32, "table", B, None)
-    dev = n_new.device
+    B, N, dev, i32 = n_new.numel(), queue.numel(), n_new.device, torch.int32
+    if table.dim() != 2:
+        raise ValueError(f"table: expected [batch, width], got {list(table.shape)}")
+    sizes = (B, 2, B + 1, max_rows, max_rows)
+    ins = (_ptr(n_new, i32, "n_new", (B,), dev), _ptr(lens, i32, "lens", (B,), dev),
+           _ptr(state, i32, "state", (2,), dev), _ptr(queue, i32, "queue", (N,), dev), N,
+           _ptr(table, i32, "table", (B, table.shape[1]), dev), B, table.shape[1], page_size, prefix_len)
     if out is None:
-        out = PagedPlan(*(torch.empty((n,), dtype=torch.int32, device=dev)
-                          for n in (B, 2, B + 1, max_rows, max_rows)))
+        out = PagedPlan(*n_new.new_empty(sum(sizes)).split_with_sizes(sizes))
+        outs = [t.data_ptr() for t in out]
     else:
-        for name, n in zip(PagedPlan._fields, (B, 2, B + 1, max_rows, max_rows)):
-            _shaped(getattr(out, name), torch.int32, "out." + name, n)
+        outs = [_ptr(t, i32, "out." + f, (n,), dev) for t, f, n in zip(out, PagedPlan._fields, sizes)]
     if ws is None:
         ws = zeros_workspace(256, dev)
-    with _together(n_new, lens=lens, state=state, queue=queue, table=table, ws=ws, out_lens=out.lens,
-                   out_state=out.state, row_start=out.row_start, slots=out.slots, pos=out.pos):
-        call("w4a_paged_plan", _p(n_new), _p(lens), _p(state), _p(queue), queue.numel(), _p(table), B, table.shape[1],
-             page_size, prefix_len, _p(out.lens), _p(out.state), _p(out.row_start), _p(out.slots), _p(out.pos),
-             max_rows, _p(ws), ws.numel(), _stream())
+    _call_on(dev, "w4a_paged_plan", *ins, *outs, max_rows, _ptr(ws, torch.uint8, "ws", ws.shape, dev), ws.numel())
     return out
 
 
@@ -593,28 +596,32 @@ def qk_prep_paged(cfg: Config, full: bool, qkv: torch.Tensor, q_gain: torch.Tens
     fp32 [rows, q_dim + 2 kv_dim] (rows may be strided), pos and slots int32
     [rows] from paged_plan (rows with slot -1 are skipped); returns q bf16
     [rows, n_heads, hd]."""
-    if qkv.dtype != torch.float32:
-        raise TypeError(f"qkv: expected {torch.float32}, got {qkv.dtype}")
-    if qkv.dim() != 2 or qkv.shape[1] != cfg.qkv_dim or qkv.stride(1) != 1:
+    nq, nkv, hd, dev, f32, bf16 = cfg.n_heads, cfg.n_kv_heads, cfg.head_dim, qkv.device, torch.float32, torch.bfloat16
+    if qkv.dtype != f32:
+        raise TypeError(f"qkv: expected {f32}, got {qkv.dtype}")
+    if not qkv.is_cuda:
+        raise ValueError("qkv: expected a CUDA tensor")
+    if qkv.dim() != 2 or qkv.shape[1] != (nq + 2 * nkv) * hd or qkv.stride(1) != 1:
         raise ValueError(f"qkv: expected [rows, {cfg.qkv_dim}] with contiguous rows")
     R = qkv.shape[0]
-    _shaped(q_gain, torch.float32, "q_gain", cfg.q_dim)
-    _shaped(k_gain, torch.float32, "k_gain", cfg.kv_dim)
-    _shaped(pos, torch.int32, "pos", R)
-    _shaped(slots, torch.int32, "slots", R)
-    _shaped(k_pages, torch.bfloat16, "k_pages", None, cfg.n_kv_heads, None, cfg.head_dim)
-    _shaped(v_pages, torch.bfloat16, "v_pages", *k_pages.shape)
+    if k_pages.dim() != 4:
+        raise ValueError(f"k_pages: expected [n_pages, n_kv, page_size, hd], got {list(k_pages.shape)}")
+    n_pages, _, page, _ = k_pages.shape
     if q_out is None:
-        q_out = torch.empty((R, cfg.n_heads, cfg.head_dim), dtype=torch.bfloat16, device=qkv.device)
-    _shaped(q_out, torch.bfloat16, "q_out", R, cfg.n_heads, cfg.head_dim)
+        q_out = torch.empty((R, nq, hd), dtype=bf16, device=dev)
     if ws is None:
-        ws = zeros_workspace(256, qkv.device)
-    c = cfg.to_c()
-    with _together(qkv, q_gain=q_gain, k_gain=k_gain, pos=pos, slots=slots, k_pages=k_pages, v_pages=v_pages, ws=ws,
-                   q_out=q_out):
-        call("w4a_qk_prep_paged", C.byref(c), 1 if full else 0, _p(qkv), qkv.stride(0), R, _p(q_gain), _p(k_gain),
-             _p(pos), _p(slots), _p(q_out), _p(k_pages), _p(v_pages), k_pages.shape[0], k_pages.shape[2], _p(ws),
-             ws.numel(), _stream())
+        ws = zeros_workspace(256, dev)
+    # a row of one has any stride
+    ld = qkv.stride(0) if R > 1 else qkv.shape[1]
+    c = _abi.W4AConfig(n_heads=nq, n_kv_heads=nkv, head_dim=hd, rope_theta=cfg.rope_theta, yarn_factor=cfg.yarn_factor,
+                       yarn_orig_ctx=cfg.yarn_orig_ctx, yarn_beta_fast=cfg.yarn_beta_fast,
+                       yarn_beta_slow=cfg.yarn_beta_slow, eps=cfg.eps)
+    _call_on(dev, "w4a_qk_prep_paged", C.byref(c), 1 if full else 0, qkv.data_ptr(), ld, R,
+             _ptr(q_gain, f32, "q_gain", (nq * hd,), dev), _ptr(k_gain, f32, "k_gain", (nkv * hd,), dev),
+             _ptr(pos, torch.int32, "pos", (R,), dev), _ptr(slots, torch.int32, "slots", (R,), dev),
+             _ptr(q_out, bf16, "q_out", (R, nq, hd), dev), _ptr(k_pages, bf16, "k_pages", (n_pages, nkv, page, hd), dev),
+             _ptr(v_pages, bf16, "v_pages", (n_pages, nkv, page, hd), dev), n_pages, page,
+             _ptr(ws, torch.uint8, "ws", ws.shape, dev), ws.numel())
     return q_out
 
 
@@ -634,29 +641,27 @@ def attn_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, r
     positions of every sequence in the pages prefix_table, read once for the
     batch.  max_new: the most rows a sequence has.  Returns bf16 [rows,
     n_heads, hd]; rows behind the last sequence are left as they were."""
-    _shaped(q, torch.bfloat16, "q", None, None, None)
-    R, nq, hd = q.shape
-    _shaped(k_pages, torch.bfloat16, "k_pages", None, None, None, hd)
-    _shaped(v_pages, torch.bfloat16, "v_pages", *k_pages.shape)
-    n_pages, nkv, page = k_pages.shape[:3]
-    B = lens.numel()
-    _shaped(lens, torch.int32, "lens", None)
-    _shaped(row_start, torch.int32, "row_start", B + 1)
-    _shaped(table, torch.int32, "table", B, None)
-    if prefix_table is not None:
-        _shaped(prefix_table, torch.int32, "prefix_table", None)
+    if q.dim() != 3 or k_pages.dim() != 4 or table.dim() != 2:
+        raise ValueError(f"expected q [rows, n_heads, hd], k_pages [n_pages, n_kv, page_size, hd] and table [batch, "
+                         f"width], got {list(q.shape)}, {list(k_pages.shape)} and {list(table.shape)}")
+    (R, nq, hd), (n_pages, nkv, page, _), B = q.shape, k_pages.shape, lens.numel()
+    dev, bf16, i32 = q.device, torch.bfloat16, torch.int32
+    if prefix_table is None:
+        prefix = 0
+    else:
+        prefix = _ptr(prefix_table, i32, "prefix_table", (prefix_table.numel(),), dev)
         if prefix_table.numel() * page < prefix_len:
             raise ValueError(f"prefix_table: {prefix_table.numel()} pages hold no {prefix_len} positions")
     if ws is None:
-        ws = attn_shared_workspace(R, B, nq, nkv, hd, max_new, q.device)
+        ws = attn_shared_workspace(R, B, nq, nkv, hd, max_new, dev)
     if out is None:
         out = torch.empty_like(q)
-    _shaped(out, torch.bfloat16, "out", R, nq, hd)
-    with _together(q, k_pages=k_pages, v_pages=v_pages, row_start=row_start, lens=lens, table=table,
-                   prefix_table=prefix_table, ws=ws, out=out):
-        call("w4a_attn_shared", _p(q), R, B, nq, nkv, hd, _p(k_pages), _p(v_pages), n_pages, page, _p(row_start),
-             _p(lens), _p(table), table.shape[1], _p(prefix_table), prefix_len, window, max_new, _p(out), _p(ws),
-             ws.numel(), _stream())
+    _call_on(dev, "w4a_attn_shared", _ptr(q, bf16, "q", (R, nq, hd), dev), R, B, nq, nkv, hd,
+             _ptr(k_pages, bf16, "k_pages", (n_pages, nkv, page, hd), dev),
+             _ptr(v_pages, bf16, "v_pages", (n_pages, nkv, page, hd), dev), n_pages, page,
+             _ptr(row_start, i32, "row_start", (B + 1,), dev), _ptr(lens, i32, "lens", (B,), dev),
+             _ptr(table, i32, "table", (B, table.shape[1]), dev), table.shape[1], prefix, prefix_len, window, max_new,
+             _ptr(out, bf16, "out", (R, nq, hd), dev), _ptr(ws, torch.uint8, "ws", ws.shape, dev), ws.numel())
     return out
 
 

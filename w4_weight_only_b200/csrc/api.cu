@@ -44,7 +44,7 @@ cudaError_t launch_paged_plan(const int32_t*, const int32_t*, const int32_t*, in
                               int32_t*, int32_t*, int32_t*, uint32_t*, int, int, int, int, int, int, cudaStream_t);
 cudaError_t launch_prep_paged(const float*, int64_t, const float*, const float*, const int32_t*, const int32_t*, int,
                               uint16_t*, uint16_t*, uint16_t*, uint32_t*, const double*, float, float, int, int, int,
-                              int, int, cudaStream_t);
+                              int, int, int, cudaStream_t);
 cudaError_t launch_attn_shared(const uint16_t*, int, int, int, int, int, const uint16_t*, const uint16_t*, int, int,
                                const int32_t*, const int32_t*, const int32_t*, int, const int32_t*, int, int, int,
                                uint16_t*, uint8_t*, int, cudaStream_t);
@@ -1224,20 +1224,31 @@ int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, int64_t 
   rc = check_pages(n_pages, page_size, nkv);
   if (rc) return rc;
   const int width = (nq + 2 * nkv) * hd;
-  if (width > 51200) return fail(W4A_ERR_SHAPE, "a QKV row of %d values (at most 51200)", width);
+  if (width > 25600) return fail(W4A_ERR_SHAPE, "a QKV row of %d values (at most 25600)", width);
   if (rows < 1) return fail(W4A_ERR_SHAPE, "rows %d", rows);
   if (ld < width || ld % 4) return fail(W4A_ERR_SHAPE, "row stride %lld (at least %d, a multiple of 4)", (long long)ld, width);
   if (!aligned16(qkv) || !aligned16(q_gain) || !aligned16(k_gain) || !aligned16(q_out) || !aligned16(k_pages) ||
       !aligned16(v_pages) || !aligned16(ws))
     return fail(W4A_ERR_ALIGN, "misaligned pointer");
   if (ws_bytes < 256) return fail(W4A_ERR_WORKSPACE, "workspace %zu < 256 bytes", ws_bytes);
-  double tab[2][64];
-  float ms[2];
-  rope_tables(cfg, tab, ms);
+  DevInfo* di;
+  rc = device_info(&di);
+  if (rc) return rc;
+  // the rotation's tables, kept while the fields they come from stay the same
+  // (64 powers take as long as the launch)
+  static thread_local W4AConfig from = {};
+  static thread_local double tab[2][64];
+  static thread_local float ms[2];
+  if (from.head_dim != hd || from.rope_theta != cfg->rope_theta || from.yarn_factor != cfg->yarn_factor ||
+      from.yarn_orig_ctx != cfg->yarn_orig_ctx || from.yarn_beta_fast != cfg->yarn_beta_fast ||
+      from.yarn_beta_slow != cfg->yarn_beta_slow) {
+    rope_tables(cfg, tab, ms);
+    from = *cfg;
+  }
   const int t = full ? 1 : 0;
   CK(launch_prep_paged(qkv, ld, q_gain, k_gain, pos, slots, rows, q_out, k_pages, v_pages,
                        static_cast<uint32_t*>(ws) + 2, tab[t], ms[t], float(cfg->eps), nq, nkv, hd, n_pages, page_size,
-                       S(stream)));
+                       di->sms, S(stream)));
   return W4A_OK;
 }
 

@@ -32,7 +32,7 @@ namespace {
 // part of the queue, the held part of the table) none of them writes.
 constexpr int PT = 512;                          // threads
 constexpr int PER = MAX_PAGED_BATCH / PT;        // sequences per thread
-constexpr int PLAN_ROWS = 8 * PT;                // rows per CTA
+constexpr int PLAN_ROWS = PT;                    // rows per CTA
 
 struct Sum3 {
   long long rows, take, freed;
@@ -70,7 +70,7 @@ struct PlanArgs {
   int32_t* slots;
   int32_t* pos;
   uint32_t* err;
-  int batch, n_queue, width, page, prefix, max_rows;
+  int batch, n_queue, width, page_log2, prefix, max_rows;
 };
 
 __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a) {
@@ -83,6 +83,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.batch + PT - 1) / PT;  // sequences of this thread, consecutive
   const int b0 = tid * per;
+  const int head = a.state[0], count = a.state[1];  // (loaded with the lengths)
   uint32_t bad = 0;
   Sum3 mine{0, 0, 0}, each[PER];
 #pragma unroll
@@ -96,7 +97,8 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a) {
       bad |= EW_BAD_SHAPE;
       continue;
     }
-    const long long held = ((long long)len + a.page - 1) / a.page, want = (end + a.page - 1) / a.page;
+    const int page1 = (1 << a.page_log2) - 1;
+    const long long held = ((long long)len + page1) >> a.page_log2, want = (end + page1) >> a.page_log2;
     if (held > a.width || want > a.width) {
       bad |= EW_PAGES;
       continue;
@@ -121,7 +123,6 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a) {
     if (w == warp) base = total;
     total = total + wsum[w];
   }
-  const int head = a.state[0], count = a.state[1];
   const long long N = a.n_queue;
   if (head < 0 || head >= N || count < 0 || count > N || count + total.freed > N)
     bad |= EW_BAD_SHAPE;
@@ -156,10 +157,11 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a) {
   const int first = blockIdx.x * PT + tid, step = gridDim.x * PT;
   // the queue in order: its live entries, then the pages freed by this call
   auto queue_page = [&](int k) {
-    if (k < count) return a.queue[(head + (long long)k) % N];
+    if (k < count) return a.queue[head + (long long)k < N ? head + k : int(head + (long long)k - N)];
     const int f = k - count, b = seq_of(free0, a.batch, f);
     return a.table[(size_t)b * a.width + (f - free0[b])];
   };
+  auto pages_of = [&](int len) { return int(((long long)len + (1 << a.page_log2) - 1) >> a.page_log2); };
   auto taken_page = [&](int k) {
     const int id = queue_page(k);
     if ((unsigned)id >= (unsigned)a.n_queue) atomicOr(a.err, EW_BAD_POS);
@@ -168,7 +170,7 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a) {
   if (ok) {
     for (int k = first; k < int(total.take); k += step) {
       const int b = seq_of(take0, a.batch, k);
-      const int held = (len0[b] + a.page - 1) / a.page;
+      const int held = pages_of(len0[b]);
       a.table[(size_t)b * a.width + held + (k - take0[b])] = taken_page(k);
     }
     for (int f = first; f < int(total.freed); f += step) {
@@ -183,12 +185,12 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a) {
     if (r < n_rows) {
       const int b = seq_of(row0, a.batch, r);
       const int own = len0[b] + (r - row0[b]);
-      const int held = (len0[b] + a.page - 1) / a.page;
-      const int j = own / a.page;
+      const int held = pages_of(len0[b]);
+      const int j = own >> a.page_log2;
       const int id = j < held ? a.table[(size_t)b * a.width + j] : queue_page(take0[b] + (j - held));
       // a page id outside the cache gives no slot: the row is not appended
       if ((unsigned)id < (unsigned)a.n_queue) {
-        slot = id * a.page + (own - j * a.page);
+        slot = (id << a.page_log2) + (own & ((1 << a.page_log2) - 1));
       } else {
         atomicOr(a.err, EW_BAD_POS);
       }
@@ -202,13 +204,16 @@ __global__ void __launch_bounds__(PT) plan_kernel(const PlanArgs a) {
 // ---------------------------------------------------------------------------
 // QK-norm over the whole projections, rotation, append into the pages
 // ---------------------------------------------------------------------------
-// One CTA per row: the row [q; k; v] (fp32) comes into shared memory by
-// asynchronous 16-byte copies, and is read there twice, for the sums of
-// squares and for the output.  The rotation of pair (i, i + hd / 2) at the row's position is
-// formed once per row while the copy is in flight: the angle in fp64,
-// reduced to [-pi, pi] there (a position of 10^5 has no fraction bits left in
-// fp32), sine and cosine in fp32.  Memory bound: 4 bytes read and 2 written
-// per element of the row.
+// A CTA takes every gridDim-th row.  The row [q; k; v] (fp32) comes into shared
+// memory by asynchronous 16-byte copies, the next one behind it while this one
+// is worked on (two buffers), and is read there twice, for the sums of squares
+// and for the output.  The rotation of pair (i, i + hd / 2) at the row's
+// position is formed once per row: the angle in fp64, reduced to [-pi, pi]
+// there (a position of 10^5 has no fraction bits left in fp32), sine and cosine
+// in fp32.  Memory bound: 4 bytes read and 2 written per element of the row;
+// three CTAs an SM keep 86 KB of a 7,168-wide row's neighbours in flight and
+// leave the gains in L1 (one CTA a row, seven an SM, read them from L2 for
+// every row: 82.7 us for 8,192 rows).
 constexpr int QT = 256;
 
 struct PrepArgs {
@@ -224,96 +229,124 @@ struct PrepArgs {
   uint32_t* err;
   double f[64];
   float ms, eps;
-  int nq, nkv, hd, n_pages, page;
+  int rows, nq, nkv, n_pages, page_log2;
 };
 
 __device__ __forceinline__ uint2 bf16x4(float a, float b, float c, float d) {
-  return make_uint2(pack_bf16x2(a, b), pack_bf16x2(c, d));
+  return make_uint2(cvt_bf16x2(a, b), cvt_bf16x2(c, d));
 }
 
-__global__ void __launch_bounds__(QT) prep_paged_kernel(const __grid_constant__ PrepArgs a) {
-  extern __shared__ __align__(16) float row[];
-  __shared__ float2 rot[64];
+template <int HD>
+__global__ void __launch_bounds__(QT, 3) prep_paged_kernel(const __grid_constant__ PrepArgs a) {
+  extern __shared__ __align__(16) float rows_sm[];
+  __shared__ float2 rot[HD / 2];
   __shared__ float red[2][QT / 32];
-  const int tid = threadIdx.x, r = blockIdx.x;
-  const int slot = a.slots[r], pos = a.pos[r];
-  if (slot == -1) return;  // a padding row: nothing read, nothing written
-  if (slot < 0 || slot >= a.n_pages * a.page || pos < 0) {
-    if (tid == 0) atomicOr(a.err, EW_BAD_POS);
-    return;
-  }
-  const int qd = a.nq * a.hd, kd = a.nkv * a.hd, h2 = a.hd / 2;
-  const float* src = a.y + r * a.ld;
-  for (int i = tid; i < (qd + 2 * kd) / 4; i += QT) cp_async16(row + 4 * i, src + 4 * i);
-  cp_async_commit();
-  if (tid >= QT - h2) {
-    const int i = tid - (QT - h2);
-    const double ang = double(pos) * a.f[i];
-    const double turn = ang - 6.283185307179586476925 * rint(ang * 0.15915494309189533577);
-    float sn, cs;
-    sincosf(float(turn), &sn, &cs);
-    rot[i] = make_float2(cs * a.ms, sn * a.ms);
-  }
-  cp_async_wait<0>();
-  __syncthreads();
-  const float4* row4 = reinterpret_cast<const float4*>(row);
-  float sq = 0.f, sk = 0.f;
-  for (int i = tid; i < qd / 4; i += QT) {
-    const float4 v = row4[i];
-    sq += (v.x * v.x + v.y * v.y) + (v.z * v.z + v.w * v.w);
-  }
-  for (int i = tid; i < kd / 4; i += QT) {
-    const float4 v = row4[qd / 4 + i];
-    sk += (v.x * v.x + v.y * v.y) + (v.z * v.z + v.w * v.w);
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    sk += __shfl_xor_sync(0xffffffffu, sk, o);
-  }
-  if ((tid & 31) == 0) {
-    red[0][tid >> 5] = sq;
-    red[1][tid >> 5] = sk;
-  }
-  __syncthreads();
-  sq = sk = 0.f;
-#pragma unroll
-  for (int w = 0; w < QT / 32; ++w) {
-    sq += red[0][w];
-    sk += red[1][w];
-  }
-  const float rq = rsqrtf(sq / float(qd) + a.eps), rk = rsqrtf(sk / float(kd) + a.eps);
-  // a thread's unit: four pairs (i .. i + 3, i + hd/2 ..) of one head
-  const int upr = h2 / 4, nu = (a.nq + a.nkv) * upr;
-  const size_t page_row = ((size_t)(slot / a.page) * a.nkv) * a.page + slot % a.page;
-  const size_t head_rows = (size_t)a.page;  // rows between the KV heads of a page
-#pragma unroll 2
-  for (int u = tid; u < nu; u += QT) {
-    const int h = u / upr, i = (u - h * upr) * 4;
-    const bool isq = h < a.nq;
-    const int c = h * a.hd + i;  // q and k lie one behind the other
-    const float rn = isq ? rq : rk;
-    const float* gain = isq ? a.qg + c : a.kg + (c - qd);
-    const float4 x1 = *reinterpret_cast<const float4*>(row + c), x2 = *reinterpret_cast<const float4*>(row + c + h2);
-    const float4 g1 = *reinterpret_cast<const float4*>(gain), g2 = *reinterpret_cast<const float4*>(gain + h2);
-    float lo[4], hi[4];
-    const float y1[4] = {x1.x * rn * g1.x, x1.y * rn * g1.y, x1.z * rn * g1.z, x1.w * rn * g1.w};
-    const float y2[4] = {x2.x * rn * g2.x, x2.y * rn * g2.y, x2.z * rn * g2.z, x2.w * rn * g2.w};
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float2 cs = rot[i + e];
-      lo[e] = y1[e] * cs.x - y2[e] * cs.y;
-      hi[e] = y2[e] * cs.x + y1[e] * cs.y;
+  const int tid = threadIdx.x;
+  constexpr int h2 = HD / 2, upr = h2 / 4;
+  const int qd = a.nq * HD, kd = a.nkv * HD, width = qd + 2 * kd;
+  const int n_slots = a.n_pages << a.page_log2;
+  auto fetch = [&](int r, int slot, float* dst) {
+    if ((unsigned)slot < (unsigned)n_slots) {
+      const float* src = a.y + r * a.ld;
+      for (int i = tid; i < width / 4; i += QT) cp_async16(dst + 4 * i, src + 4 * i);
     }
-    uint16_t* dst = isq ? a.q_out + (size_t)r * qd + c
-                        : a.k_pages + (page_row + (size_t)(h - a.nq) * head_rows) * a.hd + i;
-    *reinterpret_cast<uint2*>(dst) = bf16x4(lo[0], lo[1], lo[2], lo[3]);
-    *reinterpret_cast<uint2*>(dst + h2) = bf16x4(hi[0], hi[1], hi[2], hi[3]);
-  }
-  for (int u = tid; u < kd / 4; u += QT) {
-    const float4 v = row4[(qd + kd) / 4 + u];
-    const int h = (4 * u) / a.hd, i = 4 * u - h * a.hd;
-    *reinterpret_cast<uint2*>(a.v_pages + (page_row + (size_t)h * head_rows) * a.hd + i) = bf16x4(v.x, v.y, v.z, v.w);
+    cp_async_commit();
+  };
+  int r = blockIdx.x, buf = 0;
+  int slot = a.slots[r], pos = a.pos[r];
+  fetch(r, slot, rows_sm);
+  for (;;) {
+    const int next = r + gridDim.x;
+    int slot_n = -1, pos_n = -1;
+    if (next < a.rows) {
+      slot_n = a.slots[next];
+      pos_n = a.pos[next];
+    }
+    // (slot -1: a padding row, nothing read, nothing written)
+    const bool good = (unsigned)slot < (unsigned)n_slots && pos >= 0;
+    if (!good && slot != -1 && tid == 0) atomicOr(a.err, EW_BAD_POS);
+    if (good && tid >= QT - h2) {
+      const int i = tid - (QT - h2);
+      const double ang = double(pos) * a.f[i];
+      const double turn = ang - 6.283185307179586476925 * rint(ang * 0.15915494309189533577);
+      float sn, cs;
+      sincosf(float(turn), &sn, &cs);
+      rot[i] = make_float2(cs * a.ms, sn * a.ms);
+    }
+    float* row = rows_sm + buf * width;
+    fetch(next, slot_n, rows_sm + (buf ^ 1) * width);
+    cp_async_wait<1>();
+    __syncthreads();
+    if (good) {
+      const float4* row4 = reinterpret_cast<const float4*>(row);
+      float sq = 0.f, sk = 0.f;
+#pragma unroll 4
+      for (int i = tid; i < qd / 4; i += QT) {
+        const float4 v = row4[i];
+        sq += (v.x * v.x + v.y * v.y) + (v.z * v.z + v.w * v.w);
+      }
+      for (int i = tid; i < kd / 4; i += QT) {
+        const float4 v = row4[qd / 4 + i];
+        sk += (v.x * v.x + v.y * v.y) + (v.z * v.z + v.w * v.w);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        sk += __shfl_xor_sync(0xffffffffu, sk, o);
+      }
+      if ((tid & 31) == 0) {
+        red[0][tid >> 5] = sq;
+        red[1][tid >> 5] = sk;
+      }
+      __syncthreads();
+      sq = sk = 0.f;
+#pragma unroll
+      for (int w = 0; w < QT / 32; ++w) {
+        sq += red[0][w];
+        sk += red[1][w];
+      }
+      const float rq = rsqrtf(sq / float(qd) + a.eps), rk = rsqrtf(sk / float(kd) + a.eps);
+      // a thread's unit: four pairs (i .. i + 3, i + hd/2 ..) of one head
+      const int nu = (a.nq + a.nkv) * upr;
+      // the row's place in a page's first KV head; 1 << page_log2 rows on is the next head's
+      const size_t at = (((size_t)(slot >> a.page_log2) * a.nkv) << a.page_log2) + (slot & ((1 << a.page_log2) - 1));
+      uint16_t* k_row = a.k_pages + at * HD;
+      uint16_t* v_row = a.v_pages + at * HD;
+      uint16_t* q_row = a.q_out + (size_t)r * qd;
+#pragma unroll 3
+      for (int u = tid; u < nu; u += QT) {
+        const int h = u / upr, i = (u % upr) * 4;
+        const bool isq = h < a.nq;
+        const int c = h * HD + i;  // q and k lie one behind the other
+        const float rn = isq ? rq : rk;
+        const float* gain = isq ? a.qg + c : a.kg + (c - qd);
+        const float4 x1 = *reinterpret_cast<const float4*>(row + c), x2 = *reinterpret_cast<const float4*>(row + c + h2);
+        const float4 g1 = __ldg(reinterpret_cast<const float4*>(gain)), g2 = __ldg(reinterpret_cast<const float4*>(gain + h2));
+        float lo[4], hi[4];
+        const float y1[4] = {x1.x * rn * g1.x, x1.y * rn * g1.y, x1.z * rn * g1.z, x1.w * rn * g1.w};
+        const float y2[4] = {x2.x * rn * g2.x, x2.y * rn * g2.y, x2.z * rn * g2.z, x2.w * rn * g2.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 cs = rot[i + e];
+          lo[e] = y1[e] * cs.x - y2[e] * cs.y;
+          hi[e] = y2[e] * cs.x + y1[e] * cs.y;
+        }
+        uint16_t* dst = isq ? q_row + c : k_row + ((size_t)(h - a.nq) << a.page_log2) * HD + i;
+        *reinterpret_cast<uint2*>(dst) = bf16x4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint2*>(dst + h2) = bf16x4(hi[0], hi[1], hi[2], hi[3]);
+      }
+      for (int u = tid; u < kd / 4; u += QT) {
+        const float4 v = row4[(qd + kd) / 4 + u];
+        const int h = (4 * u) / HD, i = 4 * u - h * HD;
+        *reinterpret_cast<uint2*>(v_row + ((size_t)h << a.page_log2) * HD + i) = bf16x4(v.x, v.y, v.z, v.w);
+      }
+    }
+    if (next >= a.rows) break;
+    __syncthreads();  // the buffer, the rotation and the sums are free again
+    r = next;
+    slot = slot_n;
+    pos = pos_n;
+    buf ^= 1;
   }
 }
 
@@ -323,15 +356,16 @@ cudaError_t launch_paged_plan(const int32_t* n_new, const int32_t* lens, const i
                               int32_t* table, int32_t* lens_out, int32_t* state_out, int32_t* row_start,
                               int32_t* slots, int32_t* pos, uint32_t* err, int batch, int n_queue, int width, int page,
                               int prefix, int max_rows, cudaStream_t st) {
-  const PlanArgs a{n_new, lens,      state, queue, table, lens_out, state_out, row_start, slots,
-                   pos,   err, batch, n_queue,   width, page,  prefix, max_rows};
+  int page_log2 = 0;
+  while ((1 << page_log2) < page) ++page_log2;
+  const PlanArgs a{n_new, lens, state, queue,   table, lens_out,  state_out, row_start, slots,
+                   pos,   err,  batch, n_queue, width, page_log2, prefix,    max_rows};
   int grid = (max_rows + PLAN_ROWS - 1) / PLAN_ROWS;
-  grid = grid < 1 ? 1 : (grid > 128 ? 128 : grid);
+  grid = grid < 1 ? 1 : (grid > 592 ? 592 : grid);
   const int smem = 4 * batch * int(sizeof(int));
-  if (smem > 40 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  static SmemMark mark;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(&plan_kernel), smem, mark);
+  if (e != cudaSuccess) return e;
   plan_kernel<<<grid, PT, smem, st>>>(a);
   return cudaGetLastError();
 }
@@ -339,7 +373,7 @@ cudaError_t launch_paged_plan(const int32_t* n_new, const int32_t* lens, const i
 cudaError_t launch_prep_paged(const float* y, int64_t ld, const float* qg, const float* kg, const int32_t* pos,
                               const int32_t* slots, int rows, uint16_t* q_out, uint16_t* k_pages, uint16_t* v_pages,
                               uint32_t* err, const double* f, float ms, float eps, int nq, int nkv, int hd, int n_pages,
-                              int page, cudaStream_t st) {
+                              int page, int sms, cudaStream_t st) {
   PrepArgs a;
   a.y = y;
   a.ld = ld;
@@ -354,15 +388,23 @@ cudaError_t launch_prep_paged(const float* y, int64_t ld, const float* qg, const
   for (int i = 0; i < 64; ++i) a.f[i] = f[i];
   a.ms = ms;
   a.eps = eps;
+  a.rows = rows;
   a.nq = nq;
   a.nkv = nkv;
-  a.hd = hd;
   a.n_pages = n_pages;
-  a.page = page;
-  const int smem = (nq + 2 * nkv) * hd * 4;
-  const cudaError_t e = cudaFuncSetAttribute(prep_paged_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  a.page_log2 = 0;
+  while ((1 << a.page_log2) < page) ++a.page_log2;
+  const int smem = 2 * (nq + 2 * nkv) * hd * 4;  // two rows
+  const int grid = rows < 3 * sms ? rows : 3 * sms;
+  static SmemMark marks[2];
+  const void* fn = hd == 64 ? reinterpret_cast<const void*>(&prep_paged_kernel<64>)
+                            : reinterpret_cast<const void*>(&prep_paged_kernel<128>);
+  const cudaError_t e = allow_smem(fn, smem, marks[hd == 64 ? 0 : 1]);
   if (e != cudaSuccess) return e;
-  prep_paged_kernel<<<rows, QT, smem, st>>>(a);
+  if (hd == 64)
+    prep_paged_kernel<64><<<grid, QT, smem, st>>>(a);
+  else
+    prep_paged_kernel<128><<<grid, QT, smem, st>>>(a);
   return cudaGetLastError();
 }
 

@@ -1437,7 +1437,7 @@ ShLayout shared_layout(const ShPlan& p, int rows, int nq, int hd) {
 
 // Every launch may start before the one in front of it in the stream has
 // finished (the kernels wait for it where they need it).
-cudaError_t launch(const void* fn, dim3 grid, unsigned threads, int smem, void** args, cudaStream_t st) {
+cudaError_t launch(const void* fn, SmemMark& mark, dim3 grid, unsigned threads, int smem, void** args, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -1448,10 +1448,8 @@ cudaError_t launch(const void* fn, dim3 grid, unsigned threads, int smem, void**
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-  }
+  const cudaError_t e = allow_smem(fn, smem, mark);
+  if (e != cudaSuccess) return e;
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
@@ -1468,12 +1466,13 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
   }
   if ((e = page_map(&k64, k, HD, page, blocks, page < 64 ? page : 64)) != cudaSuccess) return e;
   if ((e = page_map(&v64, v, HD, page, blocks, page < 64 ? page : 64)) != cudaSuccess) return e;
+  static SmemMark tc_mark, few_mark[3], join_mark;
   int lead = 1;  // the call's first launch
   for (int own = 0; own < 2; ++own) {
     if (own ? !p.many : !tc_prefix) continue;
     const long long items = own ? p.own_items * a.ns_own : p.pairs * a.ns_prefix + p.rest * a.ns_rest;
     void* args[] = {&k128, &v128, &a, &own, &lead};
-    e = launch(reinterpret_cast<const void*>(&tc_kernel<HD>), dim3(unsigned(items)), TC_THREADS, Tc<HD>::SMEM, args, st);
+    e = launch(reinterpret_cast<const void*>(&tc_kernel<HD>), tc_mark, dim3(unsigned(items)), TC_THREADS, Tc<HD>::SMEM, args, st);
     if (e != cudaSuccess) return e;
     lead = 0;
   }
@@ -1487,13 +1486,13 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
                                    : reinterpret_cast<const void*>(&few_kernel<HD, 3>);
     const int smem = p.few == 16 ? F1::SMEM : (p.few == 32 ? F2::SMEM : F3::SMEM);
     const int threads = p.few == 16 ? F1::THREADS : (p.few == 32 ? F2::THREADS : F3::THREADS);
-    e = launch(fn, dim3(unsigned(a.G)), threads, smem, args, st);
+    e = launch(fn, few_mark[p.few / 16 - 1], dim3(unsigned(a.G)), threads, smem, args, st);
     if (e != cudaSuccess) return e;
   }
   // tokens per CTA of the join: one a warp when few, more where most CTAs may find nothing to do
   int tpc = a.rows <= 256 ? 8 : 64;
   void* args[] = {&a, &tpc};
-  return launch(reinterpret_cast<const void*>(&join_kernel<HD>),
+  return launch(reinterpret_cast<const void*>(&join_kernel<HD>), join_mark,
                 dim3(unsigned((a.rows + tpc - 1) / tpc), unsigned(a.nq)), JT, (2 * a.batch + 3) * 4, args, st);
 }
 

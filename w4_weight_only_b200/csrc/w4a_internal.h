@@ -4,6 +4,10 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <cuda_runtime.h>
+
+#include <atomic>
+
 #include "../../include/w4a.h"
 
 namespace w4a {
@@ -167,6 +171,23 @@ struct EngineParams {
   uint64_t* trace;
   int trace_phases;
 };
+
+// Allows a kernel `bytes` of dynamic shared memory; remembered per kernel and
+// device (mark: one per kernel), since the runtime call costs as much as a
+// launch.  Host threads may race to the same result.
+struct SmemMark {
+  std::atomic<int> bytes[64] = {};
+};
+inline cudaError_t allow_smem(const void* fn, int bytes, SmemMark& mark) {
+  if (bytes <= 40 * 1024) return cudaSuccess;  // static and dynamic together fit the default 48 KB
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && mark.bytes[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) mark.bytes[dev].store(bytes, std::memory_order_relaxed);
+  return e;
+}
 
 // Slots of a layer's ring / linear cache.
 inline int64_t kv_slots(int full, int window, int max_ctx) { return full ? max_ctx : window; }

@@ -294,6 +294,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     }
   }
 
+  // the first page ids on their way before the loads need them
+  if (warp == 8 && lane == 0 && valid > 0) {
+    const int32_t* list = own ? a.table + (size_t)b * a.width : a.ptable;
+    const int keys = own ? len : a.P;
+    prefetch_l2(list + (int((long long)keys * piece / ns) >> a.page_log2));
+  }
+
   // ---- this thread's row: token, head, its query; the visible keys [vlo,
   // vhi) (prefix positions, or own positions) ----
   const bool alt = valid <= 128;
@@ -409,6 +416,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       const uint32_t idO = umma_idesc_f16(128, HD, true) | UMMA_B_MN;
       // descriptors of the first tiles; a byte offset adds its sixteenth to the start address
       const uint64_t dQ = umma_desc_sw128(sQ, 0), dK = umma_desc_sw128(sR, 0), dV = umma_desc_mn_sw128(sR, PANEL, 1024);
+      auto plus = [](uint64_t d, uint32_t n) { return (d & 0xffffffff00000000ull) | (uint32_t(d) + n); };  // (no carry)
       int s = 0;          // the next ring slot to take
       uint32_t lap = 0;
       auto take = [&](int& slot) {
@@ -422,17 +430,17 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
         return w;
       };
       auto issue_s = [&](int qi, int ki) {
-        const uint64_t q = dQ + uint32_t((alt ? 0 : qi) * (TILE >> 4)), k = dK + uint32_t(ki * (TILE >> 4));
+        const uint64_t q = plus(dQ, uint32_t((alt ? 0 : qi) * (TILE >> 4))), k = plus(dK, uint32_t(ki * (TILE >> 4)));
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
           const uint32_t off = uint32_t((ks >> 2) * PANEL + (ks & 3) * 32) >> 4;
-          umma_f16(tmem + uint32_t(qi * 128), q + off, k + off, idS, ks > 0 ? 1u : 0u);
+          umma_f16(tmem + uint32_t(qi * 128), plus(q, off), plus(k, off), idS, ks > 0 ? 1u : 0u);
         }
         umma_commit(s_full + qi);
       };
       // O_qi (+)= P_qi V: each half of the keys when its weights are there
       auto issue_pv = [&](int qi, int vi, int j) {
-        const uint64_t v = dV + uint32_t(vi * (TILE >> 4));
+        const uint64_t v = plus(dV, uint32_t(vi * (TILE >> 4)));
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           if (!sh_wait(p_full + qi * 2 + half, uint32_t(j) & 1u, abort_flag, a.err)) return false;
@@ -441,7 +449,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           for (int k4 = 0; k4 < 4; ++k4) {
             const int ks = half * 4 + k4;
             umma_f16_ts(tmem + uint32_t(C::O_COL + qi * HD), tmem + uint32_t(C::P_COL(qi) + ks * 8),
-                        v + uint32_t(ks * 16 * 128 >> 4), idO, (j == 0 && ks == 0) ? 0u : 1u);
+                        plus(v, uint32_t(ks * 16 * 128 >> 4)), idO, (j == 0 && ks == 0) ? 0u : 1u);
           }
         }
         return true;
@@ -842,6 +850,11 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
   __syncthreads();
   if (lead) wait_previous_kernel();  // as in tc_kernel
   launch_dependents();
+  // the tables' lines on their way (two a CTA), while the lengths are read
+  if (tid < 2) {
+    const long long at = 32LL * (blockIdx.x + tid * gridDim.x), n = (long long)a.batch * a.width;
+    if (at < n) prefetch_l2(a.table + at);
+  }
   // ---- the stream and this CTA's run of it: each warp by itself, a sequence
   // a lane (the first 32 stay in registers) ----
   auto tiles_of = [&](int b, int& bad, int& first_pos) {
@@ -1179,7 +1192,8 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
 }
 
 // ---------------------------------------------------------------------------
-// join_kernel: CTA = one head and `tpc` tokens, a warp per token at a time.
+// join_kernel: CTA = one head and `tpc` tokens, `wpt` warps per token at a
+// time, each with every wpt-th piece.
 // Where a token's pieces are is worked out before the wait for them (the
 // stream's cut again, from the lengths), while they are still being made;
 // behind the wait a lane takes a piece's (m, l), then the pieces' O come in
@@ -1188,10 +1202,12 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
 constexpr int JT = 256, JCH = 8;
 
 template <int HD>
-__global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs a, const int tpc) {
+__global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs a, const int tpc, const int wpt) {
   extern __shared__ int s_start[];        // row_start [batch + 1], then the stream's tiles before each sequence
   int* cum = s_start + a.batch + 1;       // [batch + 2]
   __shared__ int s_warp[JT / 32], s_lo;
+  __shared__ float s_acc[JT / 32][HD];
+  __shared__ float2 s_ml[JT / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int head = blockIdx.y, kvh = head / a.gq, g = head - kvh * a.gq;
   if (tid == 0) {
@@ -1231,8 +1247,10 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
   const int ptiles = few_prefix_tiles(a, s_lo), px = before * a.nkv + kvh * ptiles;
   const Runs runs((before + ptiles) * a.nkv, a.G);
   bool waited = false;
-  const int tok1 = min(a.rows, int(blockIdx.x + 1) * tpc);
-  for (int tok = blockIdx.x * tpc + warp; tok < tok1; tok += JT / 32) {
+  const int tok1 = min(a.rows, int(blockIdx.x + 1) * tpc), share = warp & (wpt - 1);
+  // (with wpt > 1 a CTA has one round: tpc = JT / 32 / wpt)
+  for (int tok = blockIdx.x * tpc + warp / wpt; tok < tok1; tok += JT / 32 / wpt) {
+    if (wpt > 1 && lane == 0) s_ml[warp] = make_float2(-INFINITY, -1.f);  // nothing to join
     int b = 0, hi = a.batch;
     while (hi - b > 1) {
       const int mid = (b + hi) >> 1;
@@ -1274,16 +1292,16 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
     constexpr int E = HD / 32;
     float acc[E] = {}, L = 0.f, M = -INFINITY;
 #pragma unroll 1
-    for (int i0 = 0; i0 < total; i0 += 32) {
+    for (int i0 = 0; i0 < total; i0 += 32 * wpt) {
       // a lane's piece: where, and its weight (the address arithmetic of 32
       // pieces at once: a warp by itself takes ~5 clocks an instruction)
-      const int i = min(i0 + lane, total - 1);
+      const int i1 = i0 + lane * wpt + share, i = min(i1, total - 1);
       const bool slot = i < in_slots, mine = i < in_slots + nc;
       const size_t at = slot ? (size_t)(first + i + (i >= cut ? gap : 0)) * a.rows * a.nq + line
                              : (size_t)((mine ? c0 + i - in_slots : p0 + i - in_slots - nc) * a.few + (mine ? crow : prow));
       const float2 ml = (slot ? a.ml_part : a.ml_cont)[at];
       const float* src = (slot ? a.o_part : a.o_cont) + at * HD;
-      const bool there = i0 + lane < total && ml.y > 0.f;
+      const bool there = i1 < total && ml.y > 0.f;
       float m = there ? ml.x : -INFINITY;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -1296,7 +1314,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
       }
       const float w = there ? exp2f(ml.x - M) : 0.f;
       L = fmaf(there ? ml.y : 0.f, w, L);  // this lane's share; summed below
-      const int n32 = min(32, total - i0);
+      const int n32 = min(32, (total - i0 - share + wpt - 1) / wpt);
 #pragma unroll 1
       for (int k0 = 0; k0 < n32; k0 += JCH) {
         float x[JCH][E];
@@ -1322,12 +1340,39 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
     // the lanes' shares of L in a fixed order
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (wpt > 1) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
+      if (lane == 0) s_ml[warp] = make_float2(M, L);
+    } else {
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + line * HD + lane * E);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = cvt_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    }
+  }
+  if (!waited) wait_previous_kernel();
+  if (wpt > 1) {
+    // the shares of a token's warps, in order
+    __syncthreads();
+    const int tok = blockIdx.x * tpc + warp / wpt, w0 = warp - share;
+    if (share != 0 || tok >= tok1 || s_ml[w0].y < 0.f) return;
+    float M = -INFINITY, L = 0.f;
+    for (int w = 0; w < wpt; ++w) M = fmaxf(M, s_ml[w0 + w].x);
+    constexpr int E = HD / 32;
+    float acc[E] = {};
+    for (int w = 0; w < wpt; ++w) {
+      const float2 ml = s_ml[w0 + w];
+      const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      L = fmaf(ml.y, f, L);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(s_acc[w0 + w][lane * E + e], f, acc[e]);
+    }
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + line * HD + lane * E);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ((size_t)tok * a.nq + head) * HD + lane * E);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = cvt_bf16x2(acc[e] * inv, acc[e + 1] * inv);
   }
-  if (!waited) wait_previous_kernel();
 }
 
 // ---------------------------------------------------------------------------
@@ -1489,9 +1534,12 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
     e = launch(fn, few_mark[p.few / 16 - 1], dim3(unsigned(a.G)), threads, smem, args, st);
     if (e != cudaSuccess) return e;
   }
-  // tokens per CTA of the join: one a warp when few, more where most CTAs may find nothing to do
-  int tpc = a.rows <= 256 ? 8 : 64;
-  void* args[] = {&a, &tpc};
+  // The join: four warps a token while the (token, head) pairs do not fill the
+  // SMs, else a warp; many tokens a CTA where most CTAs may find nothing to do.
+  int wpt = (long long)a.rows * a.nq <= 16LL * sms ? 4 : 1;
+  int tpc = a.rows <= 256 ? JT / 32 / wpt : 64;
+  if (a.rows > 256) wpt = 1;
+  void* args[] = {&a, &tpc, &wpt};
   return launch(reinterpret_cast<const void*>(&join_kernel<HD>), join_mark,
                 dim3(unsigned((a.rows + tpc - 1) / tpc), unsigned(a.nq)), JT, (2 * a.batch + 3) * 4, args, st);
 }
@@ -1539,14 +1587,36 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
     if (window > 0 && keys > (long long)window + max_new + 128) keys = (long long)window + max_new + 128;
     return int((keys + 127) / 128);
   };
+  a.G = p.G;
   int unused;
   a.ns_prefix = a.ns_rest = P == 0 ? 0 : 1;
-  if (P > 0 && !a.prefix_few)
-    a.ns_prefix = pieces_for(p.pairs, p.rest, p.rest_alt, tiles(P), sms, p.prefix_cap, &a.ns_rest);
+  if (P > 0 && !a.prefix_few) {
+    // SMs for the prefix.  few_kernel's CTAs fill the others from the start,
+    // and are as many as fit there, so that all run at once:
+    //  - At most 128 rows and not many keys: bound by the launch's start and
+    //    end, so ten key tiles a CTA, 64 CTAs at least; the others are enough
+    //    to keep the memory busy.  (16 sequences behind 8,192 positions: 49 us
+    //    with all SMs for the prefix first, 37 with 64 of them.)
+    //  - Pair tiles: bound by the tensor cores, while few_kernel is bound by
+    //    memory, so two thirds of the SMs, unless the tables have room for
+    //    more own positions than the others read in that time, ~85 GB/s an SM.
+    //    (64 sequences behind 32,768: 111 us one after the other, 100 at once.)
+    int budget = sms;
+    if (p.pairs == 0 && p.rest_alt) {
+      const long long ctas = (long long)tiles(P) * nkv / 10;
+      budget = int(ctas < 64 ? 64 : (ctas < sms ? ctas : sms));
+    } else if (!p.many) {
+      const int part = sms * 2 / 3;
+      const double prefix_us = double((p.pairs + (p.rest_alt ? 0.5 : 1.0) * p.rest) * tiles(P)) * 1.95 / part;
+      const double own_us = double(batch) * width * page * nkv * hd * 4.0 / ((sms - part) * 85e3);
+      if (own_us < 1.5 * prefix_us) budget = part;
+    }
+    if (budget < sms) a.G = p.G / sms * (sms - budget);
+    a.ns_prefix = pieces_for(p.pairs, p.rest, p.rest_alt, tiles(P), budget, p.prefix_cap, &a.ns_rest);
+  }
   a.ns_own = p.many ? pieces_for(p.own_items, 0, false, tiles((long long)width * page), sms, p.own_cap, &unused) : 1;
   // one own piece a row, and little of the prefix's to read back: join in the epilogue
   a.own_joins = p.many && a.ns_own == 1 && a.ns_prefix <= 4 && a.ns_rest == a.ns_prefix;
-  a.G = p.G;
   a.scale_log2 = float(1.4426950408889634 / sqrt(double(hd)));
   return hd == 64 ? launch_shared<64>(a, k, v, p, sms, st) : launch_shared<128>(a, k, v, p, sms, st);
 }

@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 // quarter of V's columns per warp, took two barriers and 2.5 times the
 // instructions per tile, and few_kernel ran at their latency, not memory's.)
 // At a segment's end the four key quarters are joined through the stage of its
-// last tile.  The last warp loads, running ahead over segments.
+// last tile (one m-tile), or through memory of their own.  The last warp loads, running ahead over segments.
 // mma.sync, since so few rows would fill a small part of a tcgen05 tile, and
 // up to 48 rows memory bounds this kernel all the same.  Up to 16 rows the
 // tensor pipe has time to spare, and P goes in as two bf16 terms, P and its
@@ -769,11 +769,13 @@ struct Fw {
   static constexpr int ROWS = 16 * MG;
   static constexpr int NW = 4 * MG;                // math warps
   static constexpr int THREADS = 32 * (NW + 1);
-  static constexpr int PER_SM = 4 - MG;            // CTAs that are resident together
-  static constexpr int NST = (MG == 1 ? 2 : (MG == 2 ? 3 : 5)) * (HD == 128 ? 1 : 2);  // stages
+  static constexpr int PER_SM = MG == 1 ? 3 : 1;   // CTAs that are resident together
+  static constexpr int NST = (MG == 1 ? 2 : (MG == 2 ? 4 : 3)) * (HD == 128 ? 1 : 2);  // stages
+  static constexpr bool SCR = MG > 1;              // the quarters are joined in memory of their own, all m-tiles at once
   static constexpr bool LO = MG == 1;
   static constexpr int QB = ROWS * HD * 2;
-  static constexpr int SMEM = NST * 2 * KV + QB + 1024;
+  static constexpr int XB = SCR ? MG * 64 * HD * 4 : 0;
+  static constexpr int SMEM = NST * 2 * KV + QB + XB + 1024;
 };
 
 // A sequence (or the prefix, b = batch) in the tile stream.
@@ -834,8 +836,8 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
   uint8_t* sm = fw_raw + ((1024u - (smem_addr(fw_raw) & 1023u)) & 1023u);
   uint8_t* sQ = sm + NST * 2 * KV;
   __shared__ uint64_t full[NST], empty[NST];
-  __shared__ float2 s_ml[4][16];
-  __shared__ int s_vlo[ROWS], s_vhi[ROWS];
+  __shared__ float2 s_ml[C::SCR ? MG : 1][4][16];
+  __shared__ int s_vlo[ROWS], s_vhi[ROWS], s_line[ROWS];  // of a packed row: visible keys, token x n_q + head
   __shared__ int s_abort;
   volatile int* abort_flag = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -981,22 +983,12 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
       const int y = x - base * a.nkv, kvh = y / f.tiles, t0 = y - kvh * f.tiles;
       const int nt = min(x_hi - x, f.tiles - t0);
       const int nrow = f.s.n * a.gq, nmt = (nrow + 15) >> 4;
-      // ---- Q into shared memory (128-byte swizzle; zero rows up to whole
-      // m-tiles), each row's visible keys beside it ----
-      for (int i = tid; i < nmt * 16 * (HD / 8); i += NTH) {
-        const int row = i / (HD / 8), c = i - row * (HD / 8);
-        uint4 q = make_uint4(0u, 0u, 0u, 0u);
-        if (row < nrow) {
-          const int tok = row / a.gq;
-          q = *reinterpret_cast<const uint4*>(
-              a.q + ((size_t)(f.s.r0 + tok) * a.nq + kvh * a.gq + (row - tok * a.gq)) * HD + c * 8);
-        }
-        *reinterpret_cast<uint4*>(sQ + (c >> 3) * (ROWS * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = q;
-      }
+      // ---- the rows: their lines of q and of the outputs, their visible keys ----
       if (tid < nmt * 16) {
-        int vlo = 0, vhi = 0;
+        int vlo = 0, vhi = 0, line = -1;
         if (tid < nrow) {
           const int i = tid / a.gq;
+          line = (f.s.r0 + i) * a.nq + kvh * a.gq + (tid - i * a.gq);
           if (b == a.batch) {
             vhi = a.P;
             if (a.window) {
@@ -1019,6 +1011,15 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
         }
         s_vlo[tid] = vlo;
         s_vhi[tid] = vhi;
+        s_line[tid] = line;
+      }
+      math_barrier<NTH>();
+      // ---- Q into shared memory (128-byte swizzle; zero rows up to whole m-tiles) ----
+      for (int i = tid; i < nmt * 16 * (HD / 8); i += NTH) {
+        const int row = i / (HD / 8), c = i % (HD / 8), line = s_line[row];
+        uint4 q = make_uint4(0u, 0u, 0u, 0u);
+        if (line >= 0) q = *reinterpret_cast<const uint4*>(a.q + (size_t)line * HD + c * 8);
+        *reinterpret_cast<uint4*>(sQ + (c >> 3) * (ROWS * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4)) = q;
       }
       math_barrier<NTH>();
       // keys that every row sees lie in [in_lo, in_hi)
@@ -1107,7 +1108,7 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
             }
           }
         }
-        if (i + 1 < nt) {
+        if (C::SCR || i + 1 < nt) {
           __syncwarp();
           if (lane == 0) mbar_arrive(empty + st);
           if (++st == NST) {
@@ -1116,43 +1117,45 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
           }
         }
       }
-      // ---- the piece: the four key quarters of each m-tile joined through
-      // the last tile's stage, [quarter][16 rows][HD] fp32 (16-byte chunks
-      // flipped by the row), a warp then writing whole rows ----
-      float* sx = reinterpret_cast<float*>(sm + st * 2 * KV);
+      // ---- the piece: the four key quarters of each m-tile joined, [quarter]
+      // [16 rows][HD] fp32 (16-byte chunks flipped by the row), then written ----
+      float* sx = reinterpret_cast<float*>(C::SCR ? sQ + C::QB : sm + st * 2 * KV);
       const bool first = t0 == 0, whole = first && nt == f.tiles && b < a.batch && a.ns_prefix == 0;
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
         l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 2);
       }
-#pragma unroll 1
-      for (int jt = 0; jt < nmt; ++jt) {
-        math_barrier<NTH>();  // the stage has been read; the last round is over
-        if (jt == mt) {
+      math_barrier<NTH>();  // the stage has been read
+      if (busy) {
+        float* sx1 = sx + (C::SCR ? mt * 64 * HD : 0);
 #pragma unroll
-          for (int rr = 0; rr < 2; ++rr) {
-            const int row = g + 8 * rr;
-            float* d = sx + (kq * 16 + row) * HD;
+        for (int rr = 0; rr < 2; ++rr) {
+          const int row = g + 8 * rr;
+          float* d = sx1 + (kq * 16 + row) * HD;
+          // (the flip reaches bits 2 to 4 of a column: four bases, 32 columns apart from there)
 #pragma unroll
-            for (int c = 0; c < NT; ++c)
-              *reinterpret_cast<float2*>(d + ((8 * c + 2 * tq) ^ ((row & 7) << 2))) =
-                  make_float2(o[c][2 * rr], o[c][2 * rr + 1]);
-            if (tq == 0) s_ml[kq][row] = make_float2(m[rr], l[rr]);
+          for (int c1 = 0; c1 < 4; ++c1) {
+            float* d1 = d + ((8 * c1 + 2 * tq) ^ (g << 2));
+#pragma unroll
+            for (int c = c1; c < NT; c += 4)
+              *reinterpret_cast<float2*>(d1 + 8 * (c - c1)) = make_float2(o[c][2 * rr], o[c][2 * rr + 1]);
           }
+          if (tq == 0) s_ml[C::SCR ? mt : 0][kq][row] = make_float2(m[rr], l[rr]);
         }
-        math_barrier<NTH>();
+      }
+      math_barrier<NTH>();
+      {
         constexpr int CPR = HD / 4;  // 16-byte chunks of a row
-        const int items = min(16, nrow - 16 * jt) * CPR;
 #pragma unroll 2
-        for (int it = tid; it < items; it += NTH) {
-          const int row = it / CPR, c4 = it - row * CPR;
+        for (int it = tid; it < nrow * CPR; it += NTH) {
+          const int pr = it / CPR, c4 = it - pr * CPR, row = pr & 15, jt = C::SCR ? pr >> 4 : 0;
           float2 ml[4];
           float4 x[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            ml[k] = s_ml[k][row];
-            x[k] = *reinterpret_cast<const float4*>(sx + (k * 16 + row) * HD + ((c4 * 4) ^ ((row & 7) << 2)));
+            ml[k] = s_ml[jt][k][row];
+            x[k] = *reinterpret_cast<const float4*>(sx + ((jt * 4 + k) * 16 + row) * HD + ((c4 * 4) ^ ((row & 7) << 2)));
           }
           const float M = fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x));
           float L = 0.f;
@@ -1164,8 +1167,7 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
             y = make_float4(fmaf(x[k].x, f, y.x), fmaf(x[k].y, f, y.y), fmaf(x[k].z, f, y.z), fmaf(x[k].w, f, y.w));
           }
           if (!ok) continue;
-          const int pr = 16 * jt + row, tk = pr / a.gq;
-          const size_t line = (size_t)(f.s.r0 + tk) * a.nq + kvh * a.gq + (pr - tk * a.gq);
+          const size_t line = size_t(s_line[pr]);
           if (whole) {
             const float inv = L > 0.f ? 1.f / L : 0.f;
             *reinterpret_cast<uint2*>(a.out + line * HD + c4 * 4) =
@@ -1180,10 +1182,12 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
       }
       fence_proxy_async();  // the stage is refilled by tensor copies
       math_barrier<NTH>();  // and the rows' bounds and Q are free again
-      if (lane == 0) mbar_arrive(empty + st);
-      if (++st == NST) {
-        st = 0;
-        phase ^= 1;
+      if (!C::SCR) {
+        if (lane == 0) mbar_arrive(empty + st);
+        if (++st == NST) {
+          st = 0;
+          phase ^= 1;
+        }
       }
       x += nt;
     }
@@ -1461,7 +1465,7 @@ ShPlan shared_plan(int rows, int batch, int nq, int nkv, int max_new, int sms) {
   };
   p.prefix_cap = cap(p.pairs + p.rest);
   p.own_cap = p.many ? cap(p.own_items) : 1;
-  p.G = (p.few == 16 ? Fw<128, 1>::PER_SM : (p.few == 32 ? Fw<128, 2>::PER_SM : Fw<128, 3>::PER_SM)) * sms;  // CTAs that are resident together
+  p.G = (p.few == 16 ? Fw<128, 1>::PER_SM : 1) * sms;  // CTAs that are resident together
   return p;
 }
 
@@ -1592,26 +1596,35 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
   a.ns_prefix = a.ns_rest = P == 0 ? 0 : 1;
   if (P > 0 && !a.prefix_few) {
     // SMs for the prefix.  few_kernel's CTAs fill the others from the start,
-    // and are as many as fit there, so that all run at once:
-    //  - At most 128 rows and not many keys: bound by the launch's start and
-    //    end, so ten key tiles a CTA, 64 CTAs at least; the others are enough
-    //    to keep the memory busy.  (16 sequences behind 8,192 positions: 49 us
-    //    with all SMs for the prefix first, 37 with 64 of them.)
-    //  - Pair tiles: bound by the tensor cores, while few_kernel is bound by
-    //    memory, so two thirds of the SMs, unless the tables have room for
-    //    more own positions than the others read in that time, ~85 GB/s an SM.
-    //    (64 sequences behind 32,768: 111 us one after the other, 100 at once.)
+    // as many as fit there, so that all run at once: a short prefix is bound by
+    // its launch's start and end, a long one with many rows by the tensor
+    // cores, few_kernel by memory, which half of the SMs keep busy.  The split
+    // is the one with the shortest longer side, by what was measured: 12 us
+    // and 0.97 us a key tile of 128 rows for the prefix; 85 GB/s an SM, 6.5 TB/s
+    // in all, for the keys that the tables have room for (the lengths are on the
+    // device).  One after the
+    // other unless that is a tenth slower.  (16 sequences behind 8,192
+    // positions: 49 us one after the other, 36 side by side.)
     int budget = sms;
-    if (p.pairs == 0 && p.rest_alt) {
-      const long long ctas = (long long)tiles(P) * nkv / 10;
-      budget = int(ctas < 64 ? 64 : (ctas < sms ? ctas : sms));
-    } else if (!p.many) {
-      const int part = sms * 2 / 3;
-      const double prefix_us = double((p.pairs + (p.rest_alt ? 0.5 : 1.0) * p.rest) * tiles(P)) * 1.95 / part;
-      const double own_us = double(batch) * width * page * nkv * hd * 4.0 / ((sms - part) * 85e3);
-      if (own_us < 1.5 * prefix_us) budget = part;
+    if (!p.many && p.few == 16) {
+      const double unit = 0.97 * (2.0 * p.pairs + (p.rest_alt ? 1.0 : 2.0) * p.rest) * tiles(P);
+      double keys = double(width) * page;
+      if (window > 0 && keys > window + max_new) keys = window + max_new;
+      const double own_bytes = batch * keys * nkv * hd * 4.0, rate = 85e3;
+      auto prefix_us = [&](int n) { return 12.0 + unit / n; };
+      auto own_us = [&](int n) { return own_bytes / (n * rate < 6.5e6 ? n * rate : 6.5e6); };
+      double best = 0.9 * (prefix_us(sms) + own_us(sms));
+      for (int n = sms / 4; n <= sms - 8; n += 4) {
+        const double t = prefix_us(n) > own_us(sms - n) ? prefix_us(n) : own_us(sms - n);
+        if (t < best) {
+          best = t;
+          budget = n;
+        }
+      }
+      // little of the prefix, much room in the tables: half of the SMs read those as fast as all
+      if (budget == sms && unit / 64 < 12.0 && sms >= 128) budget = 64;
+      if (budget < sms) a.G = p.G / sms * (sms - budget);
     }
-    if (budget < sms) a.G = p.G / sms * (sms - budget);
     a.ns_prefix = pieces_for(p.pairs, p.rest, p.rest_alt, tiles(P), budget, p.prefix_cap, &a.ns_rest);
   }
   a.ns_own = p.many ? pieces_for(p.own_items, 0, false, tiles((long long)width * page), sms, p.own_cap, &unused) : 1;

@@ -56,6 +56,7 @@ struct ShArgs {
   int ns_rest;          // of them, for the rows behind the last whole pair tile
   int ns_own;           // pieces of the own positions in tc_kernel (slots ns_prefix ..)
   int few;              // packed rows of a sequence that few_kernel takes (16, 32 or 48)
+  int setup;            // what a segment costs besides its tiles, in tiles
   int prefix_few;       // 1: few_kernel takes the prefix too (few packed rows in all)
   int own_joins;        // 1: tc_kernel's own pieces (one each) take in the prefix's and write the output
   int G;                // CTAs of few_kernel
@@ -750,7 +751,9 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 // runs, one a CTA, whatever the lengths: a CTA takes the segments of its run
 // one by one.  A segment that lies in one run is finished there; the piece
 // with its first tile goes to the rows' own slot, a piece that begins inside a
-// segment to the CTA's (a run has one such piece at most, its first).
+// segment to the CTA's (a run has one such piece at most, its first).  A
+// segment's start and end take as long as a few tiles, so it counts for `setup`
+// tiles more, ahead of its first, which carry no keys.
 // Warp (mt, kq) of the 4 MG math warps has m-tile mt (16 rows) and keys 16 kq
 // .. + 15 of every tile, and is alone in its loop: scores by mma.sync, a softmax of its own over its keys, P straight from the score
 // fragments into the second product.  (Sharing P through shared memory, with a
@@ -783,12 +786,12 @@ struct FewSeq {
   Seq s;
   int k_lo;    // first key that a row sees
   int k_end;   // keys
-  int tiles;
+  int tiles;   // of the stream: `setup` and its key tiles
 };
 __device__ __forceinline__ int few_tiles(const ShArgs& a, const Seq& s, int* k_lo) {
   *k_lo = a.window ? max(0, s.len - s.n - a.window + 1) : 0;
   if (s.n == 0 || s.n * a.gq > a.few) return 0;
-  return ((s.len + 63) >> 6) - (*k_lo >> 6);
+  return ((s.len + 63) >> 6) - (*k_lo >> 6) + a.setup;
 }
 // The prefix as a last sequence of all rows, when there are few; first_pos:
 // the lowest position of a row (INT_MAX: no rows).
@@ -798,7 +801,7 @@ __device__ __forceinline__ int few_prefix_lo(const ShArgs& a, int first_pos) {
 __device__ __forceinline__ int few_prefix_tiles(const ShArgs& a, int first_pos) {
   if (!a.prefix_few || first_pos == 0x7fffffff) return 0;
   const int lo = few_prefix_lo(a, first_pos);
-  return lo < a.P ? ((a.P + 63) >> 6) - (lo >> 6) : 0;
+  return lo < a.P ? ((a.P + 63) >> 6) - (lo >> 6) + a.setup : 0;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -931,8 +934,8 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
         base += f.tiles;
         f = seq_at(++b);
       }
-      const int y = x - base * a.nkv, kvh = y / f.tiles, t = y - kvh * f.tiles;
-      const int nt = min(x_hi - x, f.tiles - t);
+      const int y = x - base * a.nkv, kvh = y / f.tiles, tv = y - kvh * f.tiles;
+      const int nv = min(x_hi - x, f.tiles - tv), t = max(0, tv - a.setup), nt = tv + nv - a.setup - t;
       const int32_t* pages = b == a.batch ? a.ptable : a.table + (size_t)b * a.width;
       const int bs = min(1 << a.page_log2, 64);
 #pragma unroll 1
@@ -952,7 +955,7 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
         load_tile<HD, 64>(sm + s * 2 * KV, &tmK, pages, kb, f.k_end, kvh, full + s, a, lane);
         load_tile<HD, 64>(sm + s * 2 * KV + KV, &tmV, pages, kb, f.k_end, kvh, full + s, a, lane);
       }
-      x += nt;
+      x += nv;
     }
     if (lane == 0) {
       const uint32_t first = it > uint32_t(NST) ? it - NST : 0u;
@@ -974,14 +977,16 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
     int b = b0, base = base0;
     bool ok = true;
 #pragma unroll 1
-    for (int x = x_lo; x < x_hi && ok;) {
+    for (int x = x_lo; x < x_hi;) {  // (a warp whose wait ran out goes on through the barriers, and writes nothing)
       FewSeq f = seq_at(b);
       while (x >= (base + f.tiles) * a.nkv) {
         base += f.tiles;
         f = seq_at(++b);
       }
-      const int y = x - base * a.nkv, kvh = y / f.tiles, t0 = y - kvh * f.tiles;
-      const int nt = min(x_hi - x, f.tiles - t0);
+      const int y = x - base * a.nkv, kvh = y / f.tiles, tv = y - kvh * f.tiles;
+      const int nv = min(x_hi - x, f.tiles - tv), t0 = max(0, tv - a.setup), nt = tv + nv - a.setup - t0;
+      x += nv;
+      if (nt <= 0) continue;  // only of what stands for the segment's start
       const int nrow = f.s.n * a.gq, nmt = (nrow + 15) >> 4;
       // ---- the rows: their lines of q and of the outputs, their visible keys ----
       if (tid < nmt * 16) {
@@ -1120,7 +1125,7 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
       // ---- the piece: the four key quarters of each m-tile joined, [quarter]
       // [16 rows][HD] fp32 (16-byte chunks flipped by the row), then written ----
       float* sx = reinterpret_cast<float*>(C::SCR ? sQ + C::QB : sm + st * 2 * KV);
-      const bool first = t0 == 0, whole = first && nt == f.tiles && b < a.batch && a.ns_prefix == 0;
+      const bool first = t0 == 0, whole = first && nt == f.tiles - a.setup && b < a.batch && a.ns_prefix == 0;
 #pragma unroll
       for (int rr = 0; rr < 2; ++rr) {
         l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], 1);
@@ -1189,7 +1194,6 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
           phase ^= 1;
         }
       }
-      x += nt;
     }
   }
   wait_previous_kernel();
@@ -1272,7 +1276,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
     int first = 0, in_slots = a.ns_prefix + (few ? 1 : a.ns_own), c0 = 0, nc = 0, p0 = 0, np = 0;
     if (few) {
       const int tiles = cum[b + 1] - cum[b], x = cum[b] * a.nkv + kvh * tiles;
-      c0 = runs.of(x) + 1;
+      c0 = runs.of(x + a.setup) + 1;
       nc = runs.of(x + tiles - 1) + 1 - c0;
       if (a.ns_prefix == 0 && nc == 0) continue;  // written already
     }
@@ -1281,7 +1285,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
         first = 1;  // the window ends behind the prefix: slot 0 was not written
         --in_slots;
       } else {
-        p0 = runs.of(px) + 1;
+        p0 = runs.of(px + a.setup) + 1;
         np = runs.of(px + ptiles - 1) + 1 - p0;
       }
     }
@@ -1585,6 +1589,9 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
   a.window = window;
   a.max_new = max_new;
   a.few = p.few;
+  // (24 sequences of up to 45 rows and 1,500 keys: 54 us with 0, 46 with 3, 44
+  // with 5; 16 of 5 rows and 2,048 keys: 25.0 with 0, 23.8 with 1, 23.1 with 2)
+  a.setup = p.few == 16 ? 2 : 5;
   a.prefix_few = P > 0 && rows * a.gq <= p.few;
   // key tiles that an item can have: all, or what a window reaches
   auto tiles = [&](long long keys) {

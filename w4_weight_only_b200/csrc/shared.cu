@@ -706,19 +706,39 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       constexpr int LPR = HD / 4;  // lanes of a row
       const int sub = lane / LPR, col = (lane % LPR) * 4;
       if (final) {
-#pragma unroll 4
-        for (int i = sub; i < rows; i += 32 / LPR) {
-          float4 x = *reinterpret_cast<const float4*>(sO + (w0 + i) * LD + col);
-          const float4 w = s_row[w0 + i];
-          const size_t line = size_t(__float_as_int(w.z));
-          for (int k = 0; k < np; ++k) {
-            const float2 ml = a.ml_part[k * stride + line];
-            if (!(ml.y > 0.f)) continue;
-            const float f = exp2f(ml.x - w.x) * w.y;
-            const float4 y = *reinterpret_cast<const float4*>(a.o_part + (k * stride + line) * HD + col);
-            x = make_float4(fmaf(y.x, f, x.x), fmaf(y.y, f, x.y), fmaf(y.z, f, x.z), fmaf(y.w, f, x.w));
+#pragma unroll 1
+        for (int i0 = sub; i0 < rows; i0 += 8 * (32 / LPR)) {
+          // eight rows at a time, so that the loads of the prefix's pieces overlap
+          float4 x[8], w[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            const int i = w0 + min(i0 + u * (32 / LPR), rows - 1);
+            x[u] = *reinterpret_cast<const float4*>(sO + i * LD + col);
+            w[u] = s_row[i];
           }
-          *reinterpret_cast<uint2*>(a.out + line * HD + col) = make_uint2(cvt_bf16x2(x.x, x.y), cvt_bf16x2(x.z, x.w));
+#pragma unroll 1
+          for (int k = 0; k < np; ++k) {
+            float2 ml[8];
+            float4 y[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const size_t line = k * stride + __float_as_int(w[u].z);
+              ml[u] = a.ml_part[line];
+              y[u] = *reinterpret_cast<const float4*>(a.o_part + line * HD + col);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              if (!(ml[u].y > 0.f)) continue;  // an empty piece's O was not written
+              const float f = exp2f(ml[u].x - w[u].x) * w[u].y;
+              x[u] = make_float4(fmaf(y[u].x, f, x[u].x), fmaf(y[u].y, f, x[u].y), fmaf(y[u].z, f, x[u].z),
+                                 fmaf(y[u].w, f, x[u].w));
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            if (i0 + u * (32 / LPR) < rows)
+              *reinterpret_cast<uint2*>(a.out + (size_t)__float_as_int(w[u].z) * HD + col) =
+                  make_uint2(cvt_bf16x2(x[u].x, x[u].y), cvt_bf16x2(x[u].z, x[u].w));
         }
       } else {
         float* o_part = a.o_part + part * stride * HD + col;
@@ -1543,11 +1563,13 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
     if (e != cudaSuccess) return e;
   }
   // The join: four warps a token while the (token, head) pairs do not fill the
-  // SMs, else a warp; many tokens a CTA where most CTAs may find nothing to do.
-  int wpt = (long long)a.rows * a.nq <= 16LL * sms ? 4 : 1;
-  int tpc = a.rows <= 256 ? JT / 32 / wpt : 64;
-  if (a.rows > 256) wpt = 1;
-  void* args[] = {&a, &tpc, &wpt};
+  // SMs, else a warp; many tokens a CTA only where tc_kernel has finished the
+  // long sequences, so that most find nothing to do.
+  const int wpt = a.rows <= 256 && (long long)a.rows * a.nq <= 16LL * sms ? 4 : 1;
+  long long tpc_l = (long long)a.rows * a.nq / (8LL * sms) / 8 * 8;  // about eight CTAs an SM
+  if (a.own_joins || tpc_l > 64) tpc_l = 64;
+  const int tpc = wpt > 1 ? JT / 32 / wpt : (tpc_l < 8 ? 8 : int(tpc_l));
+  void* args[] = {&a, const_cast<int*>(&tpc), const_cast<int*>(&wpt)};
   return launch(reinterpret_cast<const void*>(&join_kernel<HD>), join_mark,
                 dim3(unsigned((a.rows + tpc - 1) / tpc), unsigned(a.nq)), JT, (2 * a.batch + 3) * 4, args, st);
 }

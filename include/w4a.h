@@ -419,9 +419,10 @@ W4A_API int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, 
  * query heads per KV head, at most 2^20 rows, tables and prefix of fewer than 2^30 positions a
  * sequence and 2^37 over all tables and KV heads.  max_new: no sequence has more rows than this (it
  * sizes the work; 1 for a decode step).  prefix_table may be NULL when
- * prefix_len is 0.  Positions that no row of a sequence sees (the unwritten
- * rest of a page, keys before the window) never reach its outputs, whatever
- * the pages hold there.
+ * prefix_len is 0.  Positions that no row of the call sees (the unwritten rest
+ * of a page, keys before every window) never reach an output, whatever the
+ * pages hold there; an infinity or NaN at a position that some row sees can
+ * reach the other rows of the call too.
  * A sequence whose numbers do not fit (n > max_new, n > lens[b], lens[b] beyond
  * the table, rows outside [0, rows]) is skipped, a page id outside the cache
  * makes the outputs that read it meaningless; both are reported by w4a_check.

@@ -248,6 +248,20 @@ ATTN = [
     (16, 1, 64, 16, 65, [200], [150], 33),
     (6, 2, 128, 16, 640, [50, 0, 70], [1, 0, 1], 0),
     (7, 1, 64, 32, 64, [64], [64], 1),
+    # packed rows of 128, 129, 256, 257 (one tile, a tile and a rest, a pair, a pair and a rest)
+    (8, 2, 64, 64, 200, [70, 40], [32, 33], 0),
+    (16, 1, 128, 64, 150, [16, 17], [16, 17], 0),
+    (1, 1, 128, 16, 70, [256, 300, 257], [256, 129, 257], 0),
+    # 48 and 49 packed rows, 32 and 33, among single rows: both kernels in one call
+    (16, 1, 64, 32, 100, [50, 9, 1, 300, 2], [3, 2, 1, 4, 1], 0),
+    (1, 1, 64, 16, 90, [80, 130, 1, 64, 200, 90], [48, 49, 1, 32, 33, 17], 70),
+    # many keys, few rows: runs that cut a segment several times
+    (40, 8, 128, 64, 9, [9000], [1], 0),
+    (16, 2, 64, 128, 5000, [3, 700], [1, 4], 0),
+    # a window that hides the whole prefix from some sequences, all of it from all
+    (40, 8, 128, 64, 300, [10, 400, 100], [1, 1, 1], 64),
+    (40, 8, 128, 32, 300, [100, 400], [1, 1], 50),
+    (8, 2, 64, 16, 1000, [200] * 40, [1] * 40, 130),
 ]
 
 
@@ -262,3 +276,289 @@ def test_attention_against_oracle(api, i):
     assert torch.all(out[c["start"][-1]:] == 9.0)  # rows behind the last sequence
     again = run_attn(api, c, window, out=torch.empty_like(out))
     assert torch.equal(again[:c["start"][-1]], out[:c["start"][-1]])
+
+
+@pytest.mark.parametrize("many", [False, True])
+def test_attention_of_a_large_batch(api, many):
+    """300 sequences of 0 to 2 rows; with `many`, some of 30 to 40 among them."""
+    rng = np.random.default_rng(int(many))
+    new = [int(n) for n in rng.integers(0, 3, 300)]
+    if many:
+        for b in rng.integers(0, 300, 12):
+            new[b] = int(rng.integers(30, 41))
+    lens = [n + int(rng.integers(0, 150)) for n in new]
+    c = attn_case(300, 8, 2, 64, 16, 77, lens, new, pad=5, junk=float("inf"))
+    out = torch.full_like(c["q"], 9.0)
+    run_attn(api, c, 0, out=out)
+    close(c, out, 0)
+    assert torch.all(out[c["start"][-1]:] == 9.0)
+
+
+def test_calls_on_two_streams_at_once(api):
+    """Two attentions in flight, each with its own workspace and stream: the
+    same bits as one after the other."""
+    c = [attn_case(50 + i, 40, 8, 128, 64, 3000, [500] * 16, [1 + 2 * i] * 16) for i in range(2)]
+    ref = [run_attn(api, x) for x in c]
+    streams = [torch.cuda.Stream() for _ in c]
+    args = [(x["q"], x["k"], x["v"], i32(x["start"]), i32(x["lens"]), i32(x["table"]), i32(x["ptab"]), 3000) for x in c]
+    ws = [api.attn_shared_workspace(x["q"].shape[0], 16, 40, 8, 128, 1 + 2 * i) for i, x in enumerate(c)]
+    outs = [torch.empty_like(x["q"]) for x in c]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                api.attn_shared(*args[i], max_new=1 + 2 * i, ws=ws[i], out=outs[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        api.check(ws[i])
+        assert torch.equal(outs[i], ref[i])
+
+
+def test_attention_with_rising_scores(api):
+    """Scores that grow along the keys to 2^100 of the first one's weight: every
+    reference has to move, in the prefix and in the own positions, for few rows
+    and for many.  sum|q k| stays below 2^10, so an fp32 score is off by less
+    than 128 2^-24 2^10 / sqrt(128), a weight by less than 2^-9 of itself."""
+    for new, P in (([1, 1, 1], 700), ([3, 9, 2], 1100), ([60, 130, 1], 900)):
+        lens = [n + 200 for n in new]
+        c = attn_case(len(new), 40, 8, 128, 32, P, lens, new)
+        c["q"] = c["q"] * 0 + 1
+        flat = lambda x: x.transpose(1, 2).reshape(-1, 8, 128)
+        k = flat(c["k"]).clone()
+        for ids, n, base in [(c["ptab"], P, 0)] + [(c["table"][b], m, P) for b, m in enumerate(lens)]:
+            i = torch.arange(n, device="cuda")
+            at = i32(ids).long()[i // 32] * 32 + i % 32
+            k[at] = (k[at].float() * 0.1 + (0.0025 * (i + base) * (1 + (i % 7 == 0)))[:, None, None]).to(torch.bfloat16)
+        c["k"] = k.view(-1, 32, 8, 128).transpose(1, 2).contiguous()
+        out = run_attn(api, c)
+        ref, size = op.attend(np64(c["q"]), np64(c["k"]), np64(c["v"]), c["start"], lens, c["table"], c["ptab"], P, 0)
+        assert np.all(np.abs(np64(out) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -9) * size)
+
+
+def test_attention_one_workspace_for_many_shapes(api):
+    """A workspace of the largest call serves the others, in any order, twice."""
+    cases = [attn_case(i, *ATTN[i][:7]) for i in (5, 8, 10, 12, 5)]
+    news = [max(b - a for a, b in zip(c["start"], c["start"][1:])) for c in cases]
+    size = max(api.attn_shared_workspace(c["q"].shape[0], len(c["lens"]), 40, 8, 128, n).numel()
+               for c, n in zip(cases, news))
+    ws, outs = api.zeros_workspace(size), []
+    for _ in range(2):
+        outs.append([run_attn(api, c, ATTN[i][7], ws=ws) for c, i in zip(cases, (5, 8, 10, 12, 5))])
+    for a, b, c, i in zip(*outs, cases, (5, 8, 10, 12, 5)):
+        assert torch.equal(a, b)
+        close(c, a, ATTN[i][7])
+
+
+def test_attention_reports_numbers_that_do_not_fit(api):
+    """Rows beyond max_new, lengths beyond the table or below the rows, rows
+    outside the call: the sequence is skipped and reported, the others are as
+    without it.  A page id outside the cache is reported."""
+    from w4_weight_only_b200 import _abi
+    for hurt in ("new", "len", "short", "start", "page", "prefix page"):
+        c = attn_case(3, 40, 8, 128, 64, 200, [100, 70, 300], [1, 3, 2])
+        good = run_attn(api, c)
+        start, lens, table, ptab, mn = list(c["start"]), list(c["lens"]), [list(r) for r in c["table"]], list(c["ptab"]), 3
+        if hurt == "new":
+            mn = 2
+        elif hurt == "len":
+            lens[1] = len(table[1]) * 64 + 1
+        elif hurt == "short":
+            lens[1] = 2
+        elif hurt == "start":
+            start[3] = 7
+        elif hurt == "page":
+            table[1][1] = c["k"].shape[0]
+        else:
+            ptab[0] = -1
+        out = torch.full_like(c["q"], 9.0)
+        ws = api.attn_shared_workspace(6, 3, 40, 8, 128, 3)
+        api.attn_shared(c["q"], c["k"], c["v"], i32(start), i32(lens), i32(table), i32(ptab), 200, max_new=mn, ws=ws,
+                        out=out)
+        with pytest.raises(_abi.W4AError) as e:
+            api.check(ws)
+        assert e.value.code == _abi.ERR_KERNEL, hurt
+        if hurt in ("new", "len", "short"):
+            assert torch.equal(out[:1], good[:1]) and torch.equal(out[4:], good[4:]) and torch.all(out[1:4] == 9.0), hurt
+        elif hurt == "start":
+            assert torch.equal(out[:4], good[:4]) and torch.all(out[4:] == 9.0)
+
+
+def test_pages_past_32_bits(api):
+    """Pages whose elements lie beyond 2^31: the same bits as in a small cache."""
+    c = attn_case(7, 40, 8, 128, 64, 300, [130, 70], [2, 1])
+    good = run_attn(api, c)
+    n, far = c["k"].shape[0], 40000
+    big = dict(c)
+    for x in ("k", "v"):
+        big[x] = torch.zeros((far + n, 8, 64, 128), dtype=torch.bfloat16, device="cuda")
+        big[x][far:] = c[x]
+    big["table"] = [[p + far if p >= 0 else p for p in r] for r in c["table"]]
+    big["ptab"] = [p + far for p in c["ptab"]]
+    assert torch.equal(run_attn(api, big), good)
+    cfg = shape_config(40, 8, 128)
+    y = torch.randn((3, cfg.qkv_dim), generator=gen(1), device="cuda")
+    qg, kg = torch.ones(5120, device="cuda"), torch.ones(1024, device="cuda")
+    k0, v0 = torch.zeros_like(c["k"]), torch.zeros_like(c["k"])
+    slots = [5, 64 * (n - 1) + 63, 64]
+    api.qk_prep_paged(cfg, True, y, qg, kg, i32([4, 5, 6]), i32(slots), k0, v0)
+    ws = api.zeros_workspace(256)
+    api.qk_prep_paged(cfg, True, y, qg, kg, i32([4, 5, 6]), i32([s + 64 * far for s in slots]), big["k"], big["v"], ws=ws)
+    api.check(ws)
+    for s in slots:
+        assert torch.equal(big["k"][far + s // 64, :, s % 64], k0[s // 64, :, s % 64])
+        assert torch.equal(big["v"][far + s // 64, :, s % 64], v0[s // 64, :, s % 64])
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+class Serving:
+    """A layer of the small decoder on the paged cache: W4 QKV weights, the
+    prefix filled as a sequence of its own, then steps of a batch behind it."""
+
+    def __init__(self, api, cfg, n_pages, page, batch, seed):
+        g = gen(seed)
+        self.api, self.cfg, self.page, self.B = api, cfg, page, batch
+        self.lin = api.quantize_linear(torch.randn((cfg.qkv_dim, cfg.d_model), generator=g, device="cuda") * 0.05)
+        self.qg = 1 + 0.2 * torch.randn(cfg.q_dim, generator=g, device="cuda")
+        self.kg = 1 + 0.2 * torch.randn(cfg.kv_dim, generator=g, device="cuda")
+        self.kv = api.PagedKVCache(cfg, n_pages, page)
+        self.k, self.v = self.kv.layer_views(3)
+        self.queue, self.state = self.kv.free_queue()
+        self.ws = api.zeros_workspace(256)
+
+    def step(self, x, new, lens, table, max_rows, max_new, prefix=None, P=0, window=0, aws=None):
+        """x bf16 [rows, d] -> (plan, q, attention output)."""
+        api, cfg = self.api, self.cfg
+        p = api.paged_plan(new, lens, self.state, self.queue, table, self.page, max_rows, prefix_len=P, ws=self.ws)
+        y = torch.cat([api.gemv(self.lin, x[i:i + 16]) for i in range(0, len(x), 16)])
+        q = api.qk_prep_paged(cfg, True, y, self.qg, self.kg, p.pos, p.slots, self.k, self.v, ws=self.ws)
+        o = api.attn_shared(q, self.k, self.v, p.row_start, p.lens, table, prefix, P, window=window, max_new=max_new,
+                            ws=aws)
+        return p, q, o
+
+
+def test_a_batch_behind_a_shared_prefix(api):
+    """The prefix as a sequence, then a batch that grows, ends and is refilled
+    behind it: attention against the oracle on the device's own q and pages,
+    and against w4a_attn_decode on a private, linear copy of each history."""
+    cfg, page, P, B = wc.tiny(), 16, 85, 3
+    S = Serving(api, cfg, 40, page, B, 5)
+    g = gen(6)
+    x = lambda n: (torch.randn((n, cfg.d_model), generator=g, device="cuda")).to(torch.bfloat16)
+    ptab = torch.full((1, 8), -1, dtype=torch.int32, device="cuda")
+    p, q, o = S.step(x(P), i32([P]), i32([0]), ptab, P, P)
+    S.state = p.state
+    c = dict(q=q, k=S.k, v=S.v, start=[0, P], lens=[P], table=ptab.tolist(), ptab=[0], P=0)
+    close(c, o, 0)
+    prefix = ptab[0, :6].contiguous()
+    lens, table = i32([0] * B), torch.full((B, 6), -1, dtype=torch.int32, device="cuda")
+    kept = set(prefix.tolist())
+    for new in ([5, 20, 1], [1, 1, 1], [4, 0, 2], [1, -1, 1], [1, 7, 1], [-1, 1, -1], [9, 1, 3]):
+        rows = sum(max(n, 0) for n in new)
+        p, q, o = S.step(x(rows + 2), i32(new), lens, table, rows + 2, max(new), prefix, P)
+        api.check(S.ws)
+        lens, S.state = p.lens, p.state
+        c = dict(q=q, k=S.k, v=S.v, start=p.row_start.tolist(), lens=lens.tolist(), table=table.tolist(),
+                 ptab=prefix.tolist(), P=P)
+        close(c, o, 0)
+        # no page belongs to two
+        held = [t[j] for t, n in zip(c["table"], c["lens"]) for j in range(-(-n // page))]
+        head, count = S.state.tolist()
+        free = [S.queue.tolist()[(head + i) % 40] for i in range(count)]
+        assert sorted(held + free + list(kept)) == list(range(40))
+        # the last row of each sequence through the linear cache's attention
+        for b, n in enumerate(c["lens"]):
+            if n == 0 or new[b] < 1:
+                continue
+            i = torch.arange(P + n, device="cuda")
+            pages = torch.where(i < P, prefix[(i // page).clamp(max=5)], table[b][((i - P) // page).clamp(min=0)]).long()
+            at = torch.where(i < P, i % page, (i - P) % page)
+            kc = torch.zeros((1, 2, 256, 64), dtype=torch.bfloat16, device="cuda")
+            vc = torch.zeros_like(kc)
+            api.kv_write_region(kc, vc, 1, 2, 64, 256, 0, 0, S.k[pages, :, at].transpose(0, 1).contiguous(),
+                                S.v[pages, :, at].transpose(0, 1).contiguous())
+            r = c["start"][b + 1] - 1
+            ref = api.attn_decode(q[r:r + 1].contiguous(), kc, vc, 2, 256, i32([P + n - 1])).float()
+            # two roundings of the result and the weights' (2^-8 of sum p|v|, here <= max|v|)
+            assert torch.all((o[r].float() - ref[0]).abs() <= 2.0 ** -7 * ref[0].abs() + 2.0 ** -7 * vc.abs().max())
+
+
+def test_a_step_captured_and_replayed(api):
+    """A decode step in a CUDA graph on a side stream, replayed with other
+    lengths and tokens: the same bits as the calls made one by one."""
+    cfg, page, P, B = wc.tiny(), 16, 40, 4
+    S = Serving(api, cfg, 64, page, B, 8)
+    ptab = torch.full((1, 4), -1, dtype=torch.int32, device="cuda")
+    g = gen(9)
+    x = lambda n: (torch.randn((n, cfg.d_model), generator=g, device="cuda")).to(torch.bfloat16)
+    p, _, _ = S.step(x(P), i32([P]), i32([0]), ptab, P, P)
+    S.state = p.state
+    prefix = ptab[0, :3].contiguous()
+    table = torch.full((B, 8), -1, dtype=torch.int32, device="cuda")
+    p, _, _ = S.step(x(30), i32([10, 3, 16, 1]), i32([0] * B), table, 30, 16, prefix, P)
+    lens, state = p.lens, p.state
+    aws = api.attn_shared_workspace(B, B, cfg.n_heads, cfg.n_kv_heads, cfg.head_dim, 1)
+    xs, ones = x(B), i32([1] * B)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    snap = lambda: [t.clone() for t in (S.kv.mem, S.queue, table)]
+    keep = snap()
+    S.state = state
+    with torch.cuda.stream(side):
+        S.step(xs, ones, lens, table, B, 1, prefix, P, aws=aws)  # warm up
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            gp, gq, go = S.step(xs, ones, lens, table, B, 1, prefix, P, aws=aws)
+    torch.cuda.synchronize()
+    for t, s in zip((S.kv.mem, S.queue, table), keep):
+        t.copy_(s)
+    for _ in range(20):  # crosses page borders
+        new_x = x(B)
+        keep = snap()
+        ep, eq, eo = S.step(new_x, ones, lens.clone(), table, B, 1, prefix, P)
+        after = snap()
+        for t, s in zip((S.kv.mem, S.queue, table), keep):
+            t.copy_(s)
+        xs.copy_(new_x)
+        graph.replay()
+        torch.cuda.synchronize()
+        api.check(aws)
+        assert torch.equal(go, eo) and torch.equal(gq, eq) and torch.equal(gp.lens, ep.lens)
+        for a, b in zip(snap(), after):
+            assert torch.equal(a, b)
+        lens.copy_(gp.lens)
+        state.copy_(gp.state)
+
+
+def test_binding_refuses(api):
+    """Types, shapes, devices and layouts that the binding does not take."""
+    c = attn_case(1, 8, 2, 64, 16, 20, [9], [1])
+    a = dict(q=c["q"], k_pages=c["k"], v_pages=c["v"], row_start=i32([0, 1]), lens=i32([9]), table=i32(c["table"]),
+             prefix_table=i32(c["ptab"]), prefix_len=20)
+    api.attn_shared(**a)
+    for bad, err in ((dict(q=c["q"].half()), TypeError), (dict(q=c["q"][:, ::2]), ValueError),
+                     (dict(lens=i32([9]).long()), TypeError), (dict(row_start=i32([0, 1, 1])), ValueError),
+                     (dict(v_pages=c["v"][:-1]), ValueError), (dict(k_pages=c["k"].transpose(1, 2)), ValueError),
+                     (dict(table=i32(c["table"]).cpu()), ValueError), (dict(prefix_len=33), ValueError),
+                     (dict(table=i32(c["table"])[0]), ValueError), (dict(out=c["q"]), RuntimeError)):
+        with pytest.raises(err):
+            api.attn_shared(**{**a, **bad})
+    cfg = shape_config(8, 2, 64)
+    y, qg, kg = torch.ones((2, cfg.qkv_dim), device="cuda"), torch.ones(512, device="cuda"), torch.ones(128, device="cuda")
+    p = dict(cfg=cfg, full=True, qkv=y, q_gain=qg, k_gain=kg, pos=i32([0, 1]), slots=i32([0, 1]), k_pages=c["k"],
+             v_pages=c["v"])
+    api.qk_prep_paged(**p)
+    for bad, err in ((dict(qkv=y.half()), TypeError), (dict(qkv=y[:, 1:]), ValueError), (dict(qkv=y.cpu()), ValueError),
+                     (dict(q_gain=qg[:-1]), ValueError), (dict(slots=i32([0])), ValueError),
+                     (dict(k_pages=c["k"][0]), ValueError)):
+        with pytest.raises(err):
+            api.qk_prep_paged(**{**p, **bad})
+    n = dict(n_new=i32([1]), lens=i32([0]), state=i32([0, 2]), queue=i32([0, 1]), table=i32([[0]]), page_size=16, max_rows=1)
+    api.paged_plan(**n)
+    for bad, err in ((dict(lens=i32([0, 0])), ValueError), (dict(state=i32([0])), ValueError),
+                     (dict(table=i32([0])), ValueError), (dict(queue=i32([0, 1]).float()), TypeError),
+                     (dict(state=n["lens"].new_zeros(2).cpu()), ValueError)):
+        with pytest.raises(err):
+            api.paged_plan(**{**n, **bad})

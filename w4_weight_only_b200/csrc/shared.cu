@@ -58,6 +58,7 @@ struct ShArgs {
   int few;              // packed rows of a sequence that few_kernel takes (16, 32 or 48)
   int setup;            // what a segment costs besides its tiles, in tiles
   int prefix_few;       // 1: few_kernel takes the prefix too (few packed rows in all)
+  int with_prefix;      // 1: no pass of the prefix's own; every sequence's keys begin with it
   int own_joins;        // 1: tc_kernel's own pieces (one each) take in the prefix's and write the output
   int G;                // CTAs of few_kernel
   float scale_log2;     // log2(e) / sqrt(hd)
@@ -164,7 +165,7 @@ struct Tc {
   static constexpr int TILE = 128 * HD * 2;                 // 128 rows, bytes
   static constexpr int PANEL = 128 * 128;
   static constexpr int NT = HD == 128 ? 6 : 10;             // tiles in shared memory: Q (ALT 1, PAIR 2), the others the K / V ring
-  static constexpr int BARS = 512;
+  static constexpr int BARS = 512 + 2 * 256 * 8;            // barriers and small things, the rows' visible keys
   static constexpr int SMEM = NT * TILE + BARS + 1024;
   static constexpr int O_COL = 256;                         // O_i at 256 + i HD
   static constexpr int P_COL(int i) { return HD == 128 ? i * 128 : 384 + i * 64; }
@@ -194,6 +195,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   int* s_lo = reinterpret_cast<int*>(tbase + 2);
   int* s_b = s_lo + 1;      // sequence and its first tile
   int* s_warp = s_b + 2;    // [8]
+  // a row's visible keys [x, y) in the item's list, and in the prefix ahead of
+  // it: read once a tile, before the wait for its scores (in registers over the
+  // softmax they would spill)
+  volatile int2* s_vis = reinterpret_cast<int2*>(q_full + 64);  // [2][256]
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -297,9 +302,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 
   // the first page ids on their way before the loads need them
   if (warp == 8 && lane == 0 && valid > 0) {
-    const int32_t* list = own ? a.table + (size_t)b * a.width : a.ptable;
-    const int keys = own ? len : a.P;
-    prefetch_l2(list + (int((long long)keys * piece / ns) >> a.page_log2));
+    const bool mine = own && !a.with_prefix;
+    prefetch_l2((mine ? a.table + (size_t)b * a.width : a.ptable) +
+                (int((long long)(mine ? len : a.P) * piece / ns) >> a.page_log2));
+    if (own && a.with_prefix) prefetch_l2(a.table + (size_t)b * a.width);
   }
 
   // ---- this thread's row: token, head, its query; the visible keys [vlo,
@@ -320,14 +326,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     for (int c = 0; c < CH; ++c)
       if (!alt || (c < CH / 2) == (grp == 0)) qv[c] = src[c];
   }
-  int vlo = 0, vhi = 0, k_lo = 0, k_hi = a.P;  // k: keys that some row of the item sees
+  // vis: the row's keys of the list that the item is about; k: those that some
+  // row of the item sees.  p: the same of the prefix ahead of a sequence's own
+  // positions (its end is P)
+  int vlo = 0, vhi = 0, vlo_p = a.P, k_lo = 0, k_hi = a.P, p_lo = a.P;
   if (own) {
     k_hi = len - n + (base + valid - 1) / a.gq + 1;
-    if (a.window) k_lo = max(0, len - n + base / a.gq - a.window + 1);
+    const int back = a.window ? len - n + base / a.gq - a.window + 1 : -a.P;  // the first row's lowest key, from P on
+    k_lo = max(0, back);
+    if (a.with_prefix) p_lo = min(a.P, max(0, a.P + back));
     if (live) {
       const int p = len - n + row_tok;  // own position of the row
       vhi = p + 1;
       if (a.window) vlo = max(0, p - a.window + 1);
+      if (a.with_prefix) vlo_p = a.window ? min(a.P, max(0, a.P + p - a.window + 1)) : 0;
     }
   } else if (live) {
     vhi = a.P;
@@ -356,13 +368,23 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   }
   const uint32_t tmem = *tbase;
   int t0 = 0, nb = 0;
+  const int p_tiles = p_lo < a.P ? ((a.P + 127) >> 7) - (p_lo >> 7) : 0;
   if (k_lo < k_hi && valid > 0) {
-    const int f = k_lo >> 7, nt = ((k_hi + 127) >> 7) - f;
-    t0 = f + int((long long)nt * piece / ns);
-    nb = f + int((long long)nt * (piece + 1) / ns) - t0;
+    const int nt = p_tiles + ((k_hi + 127) >> 7) - (k_lo >> 7);
+    t0 = int((long long)nt * piece / ns);
+    nb = int((long long)nt * (piece + 1) / ns) - t0;
   }
   const int groups = valid <= 0 ? 0 : ((alt ? nb > 1 : true) ? 2 : 1);
-  const int32_t* pages = own ? a.table + (size_t)b * a.width : a.ptable;
+  // tile t of the item: where its keys are, and which of them are of use
+  struct Span {
+    const int32_t* pages;
+    int kb, lo, hi;
+  };
+  auto span = [&](int t) {
+    t += t0;
+    if (t < p_tiles) return Span{a.ptable, ((p_lo >> 7) + t) * 128, p_lo, a.P};
+    return Span{own ? a.table + (size_t)b * a.width : a.ptable, ((k_lo >> 7) + t - p_tiles) * 128, k_lo, k_hi};
+  };
 
   if (warp == 8) {
     // ---- loads, in the order in which the MMAs use them: K_0 (K_1) V_0 K_2 V_1 .. (ALT), K_0 V_0 K_1 V_1 .. (PAIR)
@@ -378,11 +400,11 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           return;
         }
       }
-      const int kb = (t0 + t) * 128;
+      const Span sp = span(t);
       const int bs = min(1 << a.page_log2, 128);
-      if (lane == 0) mbar_expect_tx(kv_full + s, load_blocks<128>(kb, k_hi, a.page_log2) * bs * HD * 2);
+      if (lane == 0) mbar_expect_tx(kv_full + s, load_blocks<128>(sp.kb, sp.hi, a.page_log2) * bs * HD * 2);
       __syncwarp();
-      load_tile<HD, 128>(sR + s * TILE, map, pages, kb, k_hi, kvh, kv_full + s, a, lane);
+      load_tile<HD, 128>(sR + s * TILE, map, sp.pages, sp.kb, sp.hi, kvh, kv_full + s, a, lane);
       if (++s == NS) {
         s = 0;
         ++lap;
@@ -511,6 +533,10 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);
+    s_vis[tid].x = vlo;
+    s_vis[tid].y = vhi;
+    s_vis[256 + tid].x = vlo_p;
+    s_vis[256 + tid].y = a.P;
     // ---- softmax ----
     const uint32_t tl = tmem + (uint32_t((warp & 3) * 32) << 16);
     const uint32_t tS = tl + uint32_t(grp * 128), tP = tl + uint32_t(C::P_COL(grp)),
@@ -522,10 +548,14 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
     if (grp < groups) {
 #pragma unroll 1
       for (int t = alt ? grp : 0; t < nb; t += alt ? 2 : 1, ++j) {
-        const int kb = (t0 + t) * 128;
+        const bool ahead = t + t0 < p_tiles;  // in the prefix ahead of the own positions
+        const int kb = (t + t0 + (ahead ? p_lo >> 7 : (k_lo >> 7) - p_tiles)) * 128;
         // keys that no row sees: their values must be finite (0 x NaN), so
         // group 0 (ALT: the tile's group) clears those rows of V
-        const bool edge = (kb < k_lo || kb + 128 > k_hi) && (alt || grp == 0);
+        const bool edge = (alt || grp == 0) && (kb < (ahead ? p_lo : k_lo) || kb + 128 > (ahead ? a.P : k_hi));
+        volatile int2* vis = s_vis + (ahead ? 256 : 0) + tid;
+        const int ilo = vis->x - kb, ihi = vis->y - kb;  // visible: ilo <= i < ihi
+        const bool part = __any_sync(0xffffffffu, live && (ilo > 0 || ihi < 128));
         if (!__all_sync(0xffffffffu, sh_wait(s_full + grp, uint32_t(j) & 1u, abort_flag, a.err))) {
           ok = false;
           break;
@@ -537,7 +567,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             ok = false;
             break;
           }
-          if (kb + r < k_lo || kb + r >= k_hi) {
+          if (kb + r < (ahead ? p_lo : k_lo) || kb + r >= (ahead ? a.P : k_hi)) {
             uint8_t* v = sR + (vi % NS) * TILE + r * 128;
 #pragma unroll
             for (int c = 0; c < HD / 8; ++c)
@@ -545,8 +575,6 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
           }
           fence_proxy_async();
         }
-        const int ilo = vlo - kb, ihi = vhi - kb;  // visible: ilo <= i < ihi
-        const bool part = __any_sync(0xffffffffu, live && (ilo > 0 || ihi < 128));
         uint32_t v[4][32];
         uint64_t sum_a = 0, sum_b = 0;
         uint64_t scale2 = 0, nref2 = 0;
@@ -807,11 +835,28 @@ struct FewSeq {
   int k_lo;    // first key that a row sees
   int k_end;   // keys
   int tiles;   // of the stream: `setup` and its key tiles
+  int p_lo;    // the same of the prefix ahead of the own positions
+  int p_tiles; // (0: none)
 };
-__device__ __forceinline__ int few_tiles(const ShArgs& a, const Seq& s, int* k_lo) {
-  *k_lo = a.window ? max(0, s.len - s.n - a.window + 1) : 0;
-  if (s.n == 0 || s.n * a.gq > a.few) return 0;
-  return ((s.len + 63) >> 6) - (*k_lo >> 6) + a.setup;
+__device__ __forceinline__ void few_tiles(const ShArgs& a, FewSeq& f) {
+  const int back = a.window ? f.s.len - f.s.n - a.window + 1 : -a.P;  // the first row's lowest key, from P on
+  f.k_lo = max(0, back);
+  f.k_end = f.s.len;
+  f.p_lo = a.with_prefix ? min(a.P, max(0, a.P + back)) : a.P;
+  f.p_tiles = f.p_lo < a.P ? ((a.P + 63) >> 6) - (f.p_lo >> 6) : 0;
+  f.tiles = f.s.n == 0 || f.s.n * a.gq > a.few
+                ? 0
+                : f.p_tiles + ((f.s.len + 63) >> 6) - (f.k_lo >> 6) + a.setup;
+}
+// Tile i of a sequence: its page list, first key, and keys of use.
+struct FewSpan {
+  const int32_t* pages;
+  int kb, lo, hi;
+};
+__device__ __forceinline__ FewSpan few_span(const ShArgs& a, const FewSeq& f, int b, int i) {
+  if (i < f.p_tiles) return FewSpan{a.ptable, ((f.p_lo >> 6) + i) * 64, f.p_lo, a.P};
+  return FewSpan{b == a.batch ? a.ptable : a.table + (size_t)b * a.width, ((f.k_lo >> 6) + i - f.p_tiles) * 64, f.k_lo,
+                 f.k_end};
 }
 // The prefix as a last sequence of all rows, when there are few; first_pos:
 // the lowest position of a row (INT_MAX: no rows).
@@ -860,7 +905,7 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
   uint8_t* sQ = sm + NST * 2 * KV;
   __shared__ uint64_t full[NST], empty[NST];
   __shared__ float2 s_ml[C::SCR ? MG : 1][4][16];
-  __shared__ int s_vlo[ROWS], s_vhi[ROWS], s_line[ROWS];  // of a packed row: visible keys, token x n_q + head
+  __shared__ int s_vlo[ROWS], s_vhi[ROWS], s_vlo_p[ROWS], s_line[ROWS];  // of a packed row: visible keys, token x n_q + head
   __shared__ int s_abort;
   volatile int* abort_flag = &s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -884,11 +929,12 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
   // a lane (the first 32 stay in registers) ----
   auto tiles_of = [&](int b, int& bad, int& first_pos) {
     if (b >= a.batch) return 0;
-    const Seq s = load_seq(a, b);
-    int lo;
-    bad |= !s.ok;
-    if (a.prefix_few && s.n > 0) first_pos = min(first_pos, a.P + s.len - s.n);
-    return few_tiles(a, s, &lo);
+    FewSeq f;
+    f.s = load_seq(a, b);
+    bad |= !f.s.ok;
+    if (a.prefix_few && f.s.n > 0) first_pos = min(first_pos, a.P + f.s.len - f.s.n);
+    few_tiles(a, f);
+    return f.tiles;
   };
   int bad = 0, first_pos = 0x7fffffff;
   const int t_first = tiles_of(lane, bad, first_pos);
@@ -933,11 +979,11 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
       f.s = Seq{0, total_rows(a), 0, 1};
       f.k_lo = p_lo;
       f.k_end = a.P;
+      f.p_lo = f.p_tiles = 0;
       f.tiles = p_tiles;
     } else {
       f.s = load_seq(a, b);
-      f.tiles = few_tiles(a, f.s, &f.k_lo);
-      f.k_end = f.s.len;
+      few_tiles(a, f);
     }
     return f;
   };
@@ -956,7 +1002,6 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
       }
       const int y = x - base * a.nkv, kvh = y / f.tiles, tv = y - kvh * f.tiles;
       const int nv = min(x_hi - x, f.tiles - tv), t = max(0, tv - a.setup), nt = tv + nv - a.setup - t;
-      const int32_t* pages = b == a.batch ? a.ptable : a.table + (size_t)b * a.width;
       const int bs = min(1 << a.page_log2, 64);
 #pragma unroll 1
       for (int i = 0; i < nt; ++i, ++it) {
@@ -969,11 +1014,11 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
             break;
           }
         }
-        const int kb = ((f.k_lo >> 6) + t + i) * 64;
-        if (lane == 0) mbar_expect_tx(full + s, 2u * load_blocks<64>(kb, f.k_end, a.page_log2) * bs * HD * 2);
+        const FewSpan sp = few_span(a, f, b, t + i);
+        if (lane == 0) mbar_expect_tx(full + s, 2u * load_blocks<64>(sp.kb, sp.hi, a.page_log2) * bs * HD * 2);
         __syncwarp();
-        load_tile<HD, 64>(sm + s * 2 * KV, &tmK, pages, kb, f.k_end, kvh, full + s, a, lane);
-        load_tile<HD, 64>(sm + s * 2 * KV + KV, &tmV, pages, kb, f.k_end, kvh, full + s, a, lane);
+        load_tile<HD, 64>(sm + s * 2 * KV, &tmK, sp.pages, sp.kb, sp.hi, kvh, full + s, a, lane);
+        load_tile<HD, 64>(sm + s * 2 * KV + KV, &tmV, sp.pages, sp.kb, sp.hi, kvh, full + s, a, lane);
       }
       x += nv;
     }
@@ -1010,7 +1055,7 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
       const int nrow = f.s.n * a.gq, nmt = (nrow + 15) >> 4;
       // ---- the rows: their lines of q and of the outputs, their visible keys ----
       if (tid < nmt * 16) {
-        int vlo = 0, vhi = 0, line = -1;
+        int vlo = 0, vhi = 0, vlo_p = a.P, line = -1;
         if (tid < nrow) {
           const int i = tid / a.gq;
           line = (f.s.r0 + i) * a.nq + kvh * a.gq + (tid - i * a.gq);
@@ -1032,8 +1077,10 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
             const int p = f.s.len - f.s.n + i;
             vhi = p + 1;
             if (a.window) vlo = max(0, p - a.window + 1);
+            if (a.with_prefix) vlo_p = a.window ? min(a.P, max(0, a.P + p - a.window + 1)) : 0;
           }
         }
+        s_vlo_p[tid] = vlo_p;
         s_vlo[tid] = vlo;
         s_vhi[tid] = vhi;
         s_line[tid] = line;
@@ -1050,6 +1097,7 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
       // keys that every row sees lie in [in_lo, in_hi)
       const int in_lo = b == a.batch ? (a.window ? a.P : 0) : (a.window ? max(0, f.s.len - a.window) : 0);
       const int in_hi = b == a.batch ? a.P : f.s.len - f.s.n + 1;
+      const int in_lo_p = a.window ? a.P + f.s.len - a.window : 0;  // (of the prefix)
       float o[NT][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
       for (int c = 0; c < NT; ++c) o[c][0] = o[c][1] = o[c][2] = o[c][3] = 0.f;
@@ -1059,11 +1107,13 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
         // (on a failed wait the warps still meet at the barriers below)
         if (!__all_sync(0xffffffffu, sh_wait(full + st, phase, abort_flag, a.err))) ok = false;
         const uint32_t sK = ring + st * 2 * KV, sV = sK + KV;
-        const int kb = ((f.k_lo >> 6) + t0 + i) * 64, k0 = kb + 16 * kq;
-        if (kb < f.k_lo || kb + 64 > f.k_end) {
+        const FewSpan sp = few_span(a, f, b, t0 + i);
+        const bool ahead = t0 + i < f.p_tiles;  // in the prefix ahead of the own positions
+        const int kb = sp.kb, k0 = kb + 16 * kq;
+        if (kb < sp.lo || kb + 64 > sp.hi) {
           // values that no row sees must be finite (0 x NaN): clear them
           const int row = lane >> 1, key = k0 + row;
-          if (key < f.k_lo || key >= f.k_end) {
+          if (key < sp.lo || key >= sp.hi) {
 #pragma unroll
             for (int c = 0; c < HD / 16; ++c) {
               const int ch = (lane & 1) * (HD / 16) + c;
@@ -1084,13 +1134,14 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
             mma_16816(s[0], qf[0], qf[1], qf[2], qf[3], kf[0], kf[1]);
             mma_16816(s[1], qf[0], qf[1], qf[2], qf[3], kf[2], kf[3]);
           }
-          const bool edge = kb < in_lo || kb + 64 > in_hi;
+          const bool edge = ahead ? kb < in_lo_p || kb + 64 > a.P : kb < in_lo || kb + 64 > in_hi;
           uint32_t ph[4], pl[4];
 #pragma unroll
           for (int rr = 0; rr < 2; ++rr) {
             float z0 = s[0][2 * rr], z1 = s[0][2 * rr + 1], z2 = s[1][2 * rr], z3 = s[1][2 * rr + 1];
             if (edge) {
-              const int row = 16 * mt + g + 8 * rr, lo = s_vlo[row] - k0 - 2 * tq, hi = s_vhi[row] - k0 - 2 * tq;
+              const int row = 16 * mt + g + 8 * rr, off = k0 + 2 * tq;
+              const int lo = (ahead ? s_vlo_p[row] : s_vlo[row]) - off, hi = (ahead ? a.P : s_vhi[row]) - off;
               z0 = (0 >= lo && 0 < hi) ? z0 : -INFINITY;
               z1 = (1 >= lo && 1 < hi) ? z1 : -INFINITY;
               z2 = (8 >= lo && 8 < hi) ? z2 : -INFINITY;
@@ -1249,11 +1300,12 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
   for (int c0 = 0; c0 < a.batch; c0 += JT) {
     int t = 0;
     if (c0 + tid < a.batch) {
-      const Seq s = load_seq(a, c0 + tid);
-      int lo;
-      t = few_tiles(a, s, &lo);
-      s_start[c0 + tid] = s.r0;
-      if (a.prefix_few && s.n > 0) atomicMin(&s_lo, a.P + s.len - s.n);
+      FewSeq f;
+      f.s = load_seq(a, c0 + tid);
+      few_tiles(a, f);
+      t = f.tiles;
+      s_start[c0 + tid] = f.s.r0;
+      if (a.prefix_few && f.s.n > 0) atomicMin(&s_lo, a.P + f.s.len - f.s.n);
     }
     int incl = t;
 #pragma unroll
@@ -1532,7 +1584,7 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
   const int64_t blocks = (int64_t)a.n_pages * a.nkv;
   CUtensorMap k128, v128, k64, v64;
   cudaError_t e;
-  const bool tc_prefix = a.P > 0 && !a.prefix_few;
+  const bool tc_prefix = a.ns_prefix > 0 && !a.prefix_few;
   if (tc_prefix || p.many) {
     if ((e = page_map(&k128, k, HD, page, blocks, page < 128 ? page : 128)) != cudaSuccess) return e;
     if ((e = page_map(&v128, v, HD, page, blocks, page < 128 ? page : 128)) != cudaSuccess) return e;
@@ -1614,7 +1666,17 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
   // (24 sequences of up to 45 rows and 1,500 keys: 54 us with 0, 46 with 3, 44
   // with 5; 16 of 5 rows and 2,048 keys: 25.0 with 0, 23.8 with 1, 23.1 with 2)
   a.setup = p.few == 16 ? 2 : 5;
-  a.prefix_few = P > 0 && rows * a.gq <= p.few;
+  // The prefix has no pass of its own where that saves nothing: few positions to
+  // read again for every sequence (a launch takes as long as 4,096 of them), or
+  // sequences that fill their row tiles by themselves (512 packed rows each on
+  // average), for which a tile with the prefix ahead of the own positions does
+  // the same work and leaves no pieces to join.  Behind a long prefix such tiles
+  // are few and long, and two passes fill the last wave better (~1,150 tokens a
+  // sequence: 3 behind 4,000 positions 430 us with a pass of the prefix, 385
+  // without; 4 behind 8,192 702 and 735).
+  const long long packed = (long long)rows * a.gq;
+  a.with_prefix = P > 0 && ((long long)batch * P <= 4096 || (packed >= 512LL * batch && P <= 4096));
+  a.prefix_few = P > 0 && !a.with_prefix && packed <= p.few;
   // key tiles that an item can have: all, or what a window reaches
   auto tiles = [&](long long keys) {
     if (window > 0 && keys > (long long)window + max_new + 128) keys = (long long)window + max_new + 128;
@@ -1622,8 +1684,8 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
   };
   a.G = p.G;
   int unused;
-  a.ns_prefix = a.ns_rest = P == 0 ? 0 : 1;
-  if (P > 0 && !a.prefix_few) {
+  a.ns_prefix = a.ns_rest = P == 0 || a.with_prefix ? 0 : 1;
+  if (a.ns_prefix > 0 && !a.prefix_few) {
     // SMs for the prefix.  few_kernel's CTAs fill the others from the start,
     // as many as fit there, so that all run at once: a short prefix is bound by
     // its launch's start and end, a long one with many rows by the tensor
@@ -1656,7 +1718,7 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
     }
     a.ns_prefix = pieces_for(p.pairs, p.rest, p.rest_alt, tiles(P), budget, p.prefix_cap, &a.ns_rest);
   }
-  a.ns_own = p.many ? pieces_for(p.own_items, 0, false, tiles((long long)width * page), sms, p.own_cap, &unused) : 1;
+  a.ns_own = p.many ? pieces_for(p.own_items, 0, false, tiles((long long)width * page + (a.with_prefix ? P : 0)), sms, p.own_cap, &unused) : 1;
   // one own piece a row, and little of the prefix's to read back: join in the epilogue
   a.own_joins = p.many && a.ns_own == 1 && a.ns_prefix <= 4 && a.ns_rest == a.ns_prefix;
   a.scale_log2 = float(1.4426950408889634 / sqrt(double(hd)));

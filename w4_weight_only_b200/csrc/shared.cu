@@ -1271,8 +1271,9 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
 }
 
 // ---------------------------------------------------------------------------
-// join_kernel: CTA = one head and `tpc` tokens, `wpt` warps per token at a
-// time, each with every wpt-th piece.
+// join_kernel: CTA = one head and `tpc` of the tokens with pieces to join (not
+// those that tc_kernel has finished), `wpt` warps per token at a time, each
+// with every wpt-th piece.
 // Where a token's pieces are is worked out before the wait for them (the
 // stream's cut again, from the lengths), while they are still being made;
 // behind the wait a lane takes a piece's (m, l), then the pieces' O come in
@@ -1282,9 +1283,9 @@ constexpr int JT = 256, JCH = 8;
 
 template <int HD>
 __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs a, const int tpc, const int wpt) {
-  extern __shared__ int s_start[];        // row_start [batch + 1], then the stream's tiles before each sequence
+  extern __shared__ int s_start[];        // tokens to join before each sequence [batch + 1], then the stream's tiles
   int* cum = s_start + a.batch + 1;       // [batch + 2]
-  __shared__ int s_warp[JT / 32], s_lo;
+  __shared__ int s_warp[JT / 32], s_tok[JT / 32], s_lo;
   __shared__ float s_acc[JT / 32][HD];
   __shared__ float2 s_ml[JT / 32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -1292,64 +1293,78 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
   if (tid == 0) {
     cum[0] = 0;
     s_lo = 0x7fffffff;
-    s_start[a.batch] = a.row_start[a.batch];
+    s_start[0] = 0;
   }
   __syncthreads();
-  int before = 0;
+  int before = 0, toks = 0;
 #pragma unroll 1
   for (int c0 = 0; c0 < a.batch; c0 += JT) {
-    int t = 0;
+    int t = 0, nt = 0;
     if (c0 + tid < a.batch) {
       FewSeq f;
       f.s = load_seq(a, c0 + tid);
       few_tiles(a, f);
       t = f.tiles;
-      s_start[c0 + tid] = f.s.r0;
+      if (!a.own_joins || f.s.n * a.gq <= a.few) nt = f.s.n;
       if (a.prefix_few && f.s.n > 0) atomicMin(&s_lo, a.P + f.s.len - f.s.n);
     }
-    int incl = t;
+    int incl = t, itok = nt;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += u;
+      const int u = __shfl_up_sync(0xffffffffu, incl, o), v = __shfl_up_sync(0xffffffffu, itok, o);
+      if (lane >= o) {
+        incl += u;
+        itok += v;
+      }
     }
-    if (lane == 31) s_warp[warp] = incl;
+    if (lane == 31) {
+      s_warp[warp] = incl;
+      s_tok[warp] = itok;
+    }
     __syncthreads();
-    int off = before;
+    incl += before;
+    itok += toks;
 #pragma unroll
     for (int w = 0; w < JT / 32; ++w) {
-      if (w < warp) off += s_warp[w];
+      if (w < warp) {
+        incl += s_warp[w];
+        itok += s_tok[w];
+      }
       before += s_warp[w];
+      toks += s_tok[w];
     }
-    if (c0 + tid < a.batch) cum[c0 + tid + 1] = off + incl;
+    if (c0 + tid < a.batch) {
+      cum[c0 + tid + 1] = incl;
+      s_start[c0 + tid + 1] = itok;
+    }
     __syncthreads();
   }
   const int ptiles = few_prefix_tiles(a, s_lo), px = before * a.nkv + kvh * ptiles;
   const Runs runs((before + ptiles) * a.nkv, a.G);
   bool waited = false;
-  const int tok1 = min(a.rows, int(blockIdx.x + 1) * tpc), share = warp & (wpt - 1);
+  int tok = 0;
+  const int x1 = min(toks, int(blockIdx.x + 1) * tpc), share = warp & (wpt - 1);
   // (with wpt > 1 a CTA has one round: tpc = JT / 32 / wpt)
-  for (int tok = blockIdx.x * tpc + warp / wpt; tok < tok1; tok += JT / 32 / wpt) {
+  for (int x = blockIdx.x * tpc + warp / wpt; x < x1; x += JT / 32 / wpt) {
     if (wpt > 1 && lane == 0) s_ml[warp] = make_float2(-INFINITY, -1.f);  // nothing to join
     int b = 0, hi = a.batch;
     while (hi - b > 1) {
       const int mid = (b + hi) >> 1;
-      if (s_start[mid] <= tok)
+      if (s_start[mid] <= x)
         b = mid;
       else
         hi = mid;
     }
     const Seq s = load_seq(a, b);
-    if (tok < s.r0 || tok >= s.r0 + s.n) continue;
+    tok = s.r0 + x - s_start[b];
     const bool few = s.n * a.gq <= a.few;
-    if (!few && a.own_joins) continue;  // finished by tc_kernel
     // the pieces: slots [first, first + in_slots), then the CTAs [c0, c0 + nc)
     // of the own positions and [p0, p0 + np) of the prefix
     int first = 0, in_slots = a.ns_prefix + (few ? 1 : a.ns_own), c0 = 0, nc = 0, p0 = 0, np = 0;
     if (few) {
-      const int tiles = cum[b + 1] - cum[b], x = cum[b] * a.nkv + kvh * tiles;
-      c0 = runs.of(x + a.setup) + 1;
-      nc = runs.of(x + tiles - 1) + 1 - c0;
+      const int tiles = cum[b + 1] - cum[b], at = cum[b] * a.nkv + kvh * tiles;
+      c0 = runs.of(at + a.setup) + 1;
+      nc = runs.of(at + tiles - 1) + 1 - c0;
       if (a.ns_prefix == 0 && nc == 0) continue;  // written already
     }
     if (a.prefix_few) {
@@ -1435,8 +1450,8 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
   if (wpt > 1) {
     // the shares of a token's warps, in order
     __syncthreads();
-    const int tok = blockIdx.x * tpc + warp / wpt, w0 = warp - share;
-    if (share != 0 || tok >= tok1 || s_ml[w0].y < 0.f) return;
+    const int x = blockIdx.x * tpc + warp / wpt, w0 = warp - share;
+    if (share != 0 || x >= x1 || s_ml[w0].y < 0.f) return;
     float M = -INFINITY, L = 0.f;
     for (int w = 0; w < wpt; ++w) M = fmaxf(M, s_ml[w0 + w].x);
     constexpr int E = HD / 32;
@@ -1615,15 +1630,18 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
     if (e != cudaSuccess) return e;
   }
   // The join: four warps a token while the (token, head) pairs do not fill the
-  // SMs, else a warp; many tokens a CTA only where tc_kernel has finished the
-  // long sequences, so that most find nothing to do.
-  const int wpt = a.rows <= 256 && (long long)a.rows * a.nq <= 16LL * sms ? 4 : 1;
-  long long tpc_l = (long long)a.rows * a.nq / (8LL * sms) / 8 * 8;  // about eight CTAs an SM
-  if (a.own_joins || tpc_l > 64) tpc_l = 64;
+  // SMs, else a warp.
+  // The tokens that may have pieces: all, or those of sequences with few rows
+  // (one prompt of 8,192: 714 us with a grid over all of them, 669 over nine).
+  const long long most = (long long)a.batch * (a.few / a.gq);
+  const int toks = a.own_joins && most < a.rows ? int(most) : a.rows;
+  const int wpt = toks <= 256 && (long long)toks * a.nq <= 16LL * sms ? 4 : 1;
+  long long tpc_l = (long long)toks * a.nq / (8LL * sms) / 8 * 8;  // about eight CTAs an SM
+  if (tpc_l > 64) tpc_l = 64;
   const int tpc = wpt > 1 ? JT / 32 / wpt : (tpc_l < 8 ? 8 : int(tpc_l));
   void* args[] = {&a, const_cast<int*>(&tpc), const_cast<int*>(&wpt)};
   return launch(reinterpret_cast<const void*>(&join_kernel<HD>), join_mark,
-                dim3(unsigned((a.rows + tpc - 1) / tpc), unsigned(a.nq)), JT, (2 * a.batch + 3) * 4, args, st);
+                dim3(unsigned((toks + tpc - 1) / tpc), unsigned(a.nq)), JT, (2 * a.batch + 3) * 4, args, st);
 }
 
 }  // namespace

@@ -318,13 +318,20 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
   const bool live = warp < 8 && prow < base + valid;
   const int row_tok = live ? prow / a.gq : 0;
   const int tok = r0 + row_tok, head = kvh * a.gq + (live ? prow - row_tok * a.gq : 0);
-  constexpr int CH = HD / 8;  // 16-byte chunks of a row (ALT: each group brings half of them)
-  uint4 qv[CH];
-  if (live) {
-    const uint4* src = reinterpret_cast<const uint4*>(a.q + ((size_t)tok * a.nq + head) * HD);
+  constexpr int CH = HD / 8, RPI = 32 / CH;  // 16-byte chunks of a row, rows a warp brings at a time
+  if (warp < 8) {
+    // The rows of Q into shared memory (128-byte swizzle), each warp its 32, a
+    // row's chunks side by side (a row per thread took 7,000 clocks; ALT: each
+    // group brings every second round).  Dead rows keep what was there.
+    const int line = live ? tok * a.nq + head : -1;
+    uint8_t* dst = sQ + (alt ? 0 : grp) * TILE + (warp & 3) * 32 * 128;
+    const int c = lane % CH;
 #pragma unroll
-    for (int c = 0; c < CH; ++c)
-      if (!alt || (c < CH / 2) == (grp == 0)) qv[c] = src[c];
+    for (int i = 0; i < CH; ++i) {
+      const int row = i * RPI + lane / CH, at = __shfl_sync(0xffffffffu, line, row);
+      if (at >= 0 && (!alt || (i & 1) == grp))
+        cp_async16(dst + (c >> 3) * PANEL + row * 128 + (((c & 7) ^ (row & 7)) << 4), a.q + (size_t)at * HD + c * 8);
+    }
   }
   // vis: the row's keys of the list that the item is about; k: those that some
   // row of the item sees.  p: the same of the prefix ahead of a sequence's own
@@ -522,14 +529,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       sh_drain(o_done, 0u, a.err);
     }
   } else {
-    // ---- the rows of Q into shared memory (128-byte swizzle; ALT: half of each row per group) ----
-    if (live) {
-      uint8_t* dst = sQ + (alt ? 0 : grp) * TILE + r * 128;
-#pragma unroll
-      for (int c = 0; c < CH; ++c)
-        if (!alt || (c < CH / 2) == (grp == 0))
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * PANEL + (((c & 7) ^ (r & 7)) << 4)) = qv[c];
-    }
+    cp_async_wait<0>();
     fence_proxy_async();
     __syncwarp();
     if (lane == 0) mbar_arrive(q_full);

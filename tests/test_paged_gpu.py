@@ -314,6 +314,20 @@ def test_calls_on_two_streams_at_once(api):
         assert torch.equal(outs[i], ref[i])
 
 
+@pytest.mark.parametrize("P,new,more", [
+    (8192, [1300, 743, 855, 824], 200), (1000, [1300, 700, 900], 0), (0, [4000], 0), (8192, [1] * 16, 1500),
+    (4097, [9, 7, 8, 5] * 6, 900)])
+def test_inputs_that_no_cache_holds(api, P, new, more):
+    """The first call, every input in memory only, gives the bits of the second."""
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for seed in range(2):
+        c = attn_case(seed, 40, 8, 128, 64, P, [n + more for n in new], new)
+        flush.zero_()
+        first = run_attn(api, c)
+        assert torch.isfinite(first).all()
+        assert torch.equal(first, run_attn(api, c))
+
+
 def test_attention_with_rising_scores(api):
     """Scores that grow along the keys to 2^100 of the first one's weight: every
     reference has to move, in the prefix and in the own positions, for few rows

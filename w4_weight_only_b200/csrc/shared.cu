@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
       if (at >= 0 && (!alt || (i & 1) == grp))
         cp_async16(dst + (c >> 3) * PANEL + row * 128 + (((c & 7) ^ (row & 7)) << 4), a.q + (size_t)at * HD + c * 8);
     }
+    cp_async_commit();
   }
   // vis: the row's keys of the list that the item is about; k: those that some
   // row of the item sees.  p: the same of the prefix ahead of a sequence's own

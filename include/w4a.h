@@ -411,14 +411,16 @@ W4A_API int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, 
  * of its lens[b] own positions (lens after the step's append, the plan's
  * lens_out), is at position p = prefix_len + lens[b] - n + i and sees the
  * positions j <= p, with window > 0 only those with p - j < window; the
- * prefix's from prefix_table, read once for the batch, its own from table[b].
+ * prefix's from prefix_table, read once for the batch (a short one with each
+ * sequence's own, where that is faster), its own from table[b].
  * out[r] bf16 [n_heads, head_dim] = softmax(q k / sqrt(head_dim)) v, query head
  * h over KV head h / (n_heads / n_kv_heads).
  * q, out: bf16 [rows, n_heads, head_dim]; rows from row_start[batch] on are
  * neither read nor written.  head_dim 64 or 128, at most 64 KV heads and 16
- * query heads per KV head, at most 2^20 rows, tables and prefix of fewer than 2^30 positions a
- * sequence and 2^37 over all tables and KV heads.  max_new: no sequence has more rows than this (it
- * sizes the work; 1 for a decode step).  prefix_table may be NULL when
+ * query heads per KV head, at most 2^20 rows, tables and prefix of fewer than
+ * 2^30 positions a sequence and 2^37 over all tables and KV heads.  max_new: no
+ * sequence has more rows than this (it sizes the work; 1 for a decode step).
+ * prefix_table may be NULL when
  * prefix_len is 0.  Positions that no row of the call sees (the unwritten rest
  * of a page, keys before every window) never reach an output, whatever the
  * pages hold there; an infinity or NaN at a position that some row sees can

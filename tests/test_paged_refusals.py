@@ -76,6 +76,13 @@ def test_attn_refusals(lib, kw, code):
     assert lib.w4a_attn_shared(*attn_args(**kw)) == getattr(_abi, "ERR_" + code)
 
 
+def test_attn_refuses_tables_that_fit_only_without_the_prefix(lib):
+    """4,096 tables of 8,182 pages of 64 over 64 KV heads: 2^31 tiles of 64 keys
+    with a prefix of 4,096 ahead of each."""
+    big = dict(batch=4096, nq=64, nkv=64, page=64, width=8182, rows=1 << 20)
+    assert lib.w4a_attn_shared(*attn_args(**big, P_=4096)) == _abi.ERR_SHAPE
+
+
 def test_sizes(lib):
     out = C.c_size_t(0)
     c = config.tiny().to_c()

@@ -638,8 +638,8 @@ def attn_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, r
     """Attention of a step's rows q bf16 [rows, n_heads, hd] over one layer's
     pages [n_pages, n_kv, page_size, hd] (w4a_attn_shared): row_start [B + 1]
     and lens [B] from paged_plan, table [B, width]; the first prefix_len
-    positions of every sequence in the pages prefix_table, read once for the
-    batch.  max_new: the most rows a sequence has.  Returns bf16 [rows,
+    positions of every sequence in the pages prefix_table, a long prefix read
+    once for the batch.  max_new: the most rows a sequence has.  Returns bf16 [rows,
     n_heads, hd]; rows behind the last sequence are left as they were."""
     if q.dim() != 3 or k_pages.dim() != 4 or table.dim() != 2:
         raise ValueError(f"expected q [rows, n_heads, hd], k_pages [n_pages, n_kv, page_size, hd] and table [batch, "

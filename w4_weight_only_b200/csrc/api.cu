@@ -1289,7 +1289,9 @@ int w4a_attn_shared(const uint16_t* q, int rows, int batch, int n_heads, int n_k
   if (window < 0) return fail(W4A_ERR_SHAPE, "window %d", window);
   if (table_width < 1 || (long long)table_width * page_size >= (1LL << 30))
     return fail(W4A_ERR_SHAPE, "table_width %d (fewer than 2^30 positions)", table_width);
-  const long long tiles = (long long)batch * ((long long)table_width * page_size / 64 + 8) + prefix_len / 64 + 8;
+  // 64-key tiles of all sequences (a prefix of up to 4,096 positions may be read with each)
+  const long long ahead = prefix_len < 4096 ? prefix_len : 4096;
+  const long long tiles = batch * (((long long)table_width * page_size + ahead) / 64 + 10) + prefix_len / 64 + 8;
   if (tiles * n_kv_heads > 0x7fffffffLL)
     return fail(W4A_ERR_SHAPE, "tables of %d x %d pages (at most 2^37 positions over the KV heads)", batch, table_width);
   if (!aligned16(q) || !aligned16(k_pages) || !aligned16(v_pages) || !aligned16(out) || !aligned16(ws))

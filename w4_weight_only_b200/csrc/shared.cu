@@ -10,18 +10,30 @@
 // A softmax over a union of key ranges is the join of the softmaxes over the
 // ranges: each piece keeps a reference m (log2 units), l = sum 2^(s - m) and
 // O = sum 2^(s - m) v in fp32, and pieces join as sum O 2^(m - M) /
-// sum l 2^(m - M).  So the work is cut twice: the prefix apart from the own
-// positions, because all rows share its keys, and both along the keys, to
-// fill the SMs when there are few rows.
+// sum l 2^(m - M).  So the work is cut twice: a long prefix apart from the own
+// positions, because all rows share its keys (a short one is read ahead of
+// each sequence's own, see with_prefix), and both along the keys, to fill the
+// SMs when there are few rows.
 //
 //  - tc_kernel: tcgen05, tiles of 128 packed rows (row x query heads of one
 //    KV head) by 128 keys.  The prefix for all rows of the batch, and the own
 //    positions of the sequences with many rows.
-//  - few_kernel: mma.sync, at most 16 packed rows: the own positions of the
-//    sequences with few rows (decode), read at memory speed.
-//  - join_kernel: joins the pieces of each (row, head).
+//  - few_kernel: mma.sync, sequences with at most 16, 32 or 48 packed rows
+//    (decode, a few drafted tokens): their own positions, read at memory speed.
+//  - join_kernel: joins the pieces of each (row, head) that tc_kernel has not
+//    finished itself.
 // They are launched one behind the other and overlap (each may start when the
-// one before has started); the join waits for all.
+// one before has started); what reads a piece waits for the launch before.
+//
+// Measured, 40 query heads over 8 of K / V, head_dim 128, GPU time of a call in
+// a full queue (a call that finds the queue empty takes the host's 12 to 16 us
+// at least):
+//   a prompt of 8,192: 636 us, 1,080 TFLOP/s (softmax and tensor core in turn)
+//   3,722 rows of 4 sequences behind 8,192 positions: 658 us, 1,050 TFLOP/s
+//   16 sequences of one row, up to 16,384 own positions: 97 us, 6.2 TB/s
+//   16 of one row and up to 2,048 behind 8,192: 36 us
+//   64 of one row and up to 1,024 behind 32,768: 102 us, 430 TFLOP/s
+//   24 of 5 to 9 rows and up to 1,500 behind 4,097, pages of 16: 86 us
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -150,16 +162,23 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* map, 
 //  ALT (at most 128 rows): one tile of rows, group i has the key tiles of
 //        parity i, and the groups' pieces are joined at the end.  A key tile
 //        takes half of PAIR's time.
-// S_i = Q K^T into TMEM columns [128 i, + 128); the group reads its rows twice
-// (32 columns at a time: the maximum, then the weights; a second read of TMEM
-// costs less than 128 registers and four times the code), forms P = 2^(s - m)
-// and writes it back as bf16 pairs over the first 64 of the same columns
-// (head_dim 64: next to O), where the second MMA reads it as its A operand,
-// O_i += P V, V as an MN-major operand; it starts on the first 64 keys while
-// the weights of the others are formed.  The reference m moves only when the
-// maximum has risen by more than 2^8 over it, so O is rescaled rarely; P <=
-// 2^8 is rounded to bf16, 2^-8 of each weight at most, while l sums the
-// weights unrounded in fp32.
+// S_i = Q K^T into TMEM columns [128 i, + 128); a thread takes its row's 128
+// scores into registers at once, forms P = 2^(s - m) and writes it back as bf16
+// pairs over the first 64 of the same columns (head_dim 64: next to O), where
+// the second MMA reads it as its A operand, O_i += P V, V as an MN-major
+// operand; it starts on the first 64 keys while the weights of the others are
+// formed.  The reference m moves only when the maximum has risen by more than
+// 2^8 over it, so O is rescaled rarely; P <= 2^8 is rounded to bf16, 2^-8 of
+// each weight at most, while l sums the weights unrounded in fp32.
+// What bounds it: a pair of tiles takes ~3,650 clocks a step of 128 keys,
+// against 2,140 of the tensor core alone: a group's softmax (~2,000) and the
+// latency of its two MMAs (~1,650) follow one another, and the other group's
+// fill only part of that.  48 % of the tensor pipe's cycles are busy over a
+// prompt of 8,192, 50 % of the special-function unit's.  An item's start and
+// end take ~10,000 clocks more, so items are long where there are enough rows.
+// Slower were: S in two halves of 64 keys, twice as many softmax warps, waits
+// that spin instead of sleep, items handed out by a counter, and loads that
+// start ahead of the rows' part of an item's start.
 template <int HD>
 struct Tc {
   static constexpr int TILE = 128 * HD * 2;                 // 128 rows, bytes
@@ -804,16 +823,19 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 // segment's start and end take as long as a few tiles, so it counts for `setup`
 // tiles more, ahead of its first, which carry no keys.
 // Warp (mt, kq) of the 4 MG math warps has m-tile mt (16 rows) and keys 16 kq
-// .. + 15 of every tile, and is alone in its loop: scores by mma.sync, a softmax of its own over its keys, P straight from the score
-// fragments into the second product.  (Sharing P through shared memory, with a
-// quarter of V's columns per warp, took two barriers and 2.5 times the
-// instructions per tile, and few_kernel ran at their latency, not memory's.)
-// At a segment's end the four key quarters are joined through the stage of its
-// last tile (one m-tile), or through memory of their own.  The last warp loads, running ahead over segments.
-// mma.sync, since so few rows would fill a small part of a tcgen05 tile, and
-// up to 48 rows memory bounds this kernel all the same.  Up to 16 rows the
-// tensor pipe has time to spare, and P goes in as two bf16 terms, P and its
-// rounding error, for two products; above rounded to bf16 once.
+// .. + 15 of every tile, and is alone in its loop: scores by mma.sync, a
+// softmax of its own over its keys, P straight from the score fragments into
+// the second product.  (Sharing P through shared memory, with a quarter of V's
+// columns per warp, took two barriers and 2.5 times the instructions per tile,
+// and few_kernel ran at their latency, not memory's.)  At a segment's end the
+// four key quarters are joined through the stage of its last tile (one
+// m-tile), or through memory of their own.  The last warp loads, running ahead
+// over segments.  mma.sync, since so few rows would fill a small part of a
+// tcgen05 tile, and memory bounds this kernel all the same: 16 sequences of
+// up to 16,384 positions (600 MB) take 97 us, 6.2 TB/s, one of 65,536 51 us,
+// 5.3 TB/s; its start and end are ~8 us of each.  Up to 16 rows the tensor pipe
+// has time to spare, and P goes in as two bf16 terms, P and its rounding
+// error, for two products; above rounded to bf16 once.
 template <int HD, int MG>
 struct Fw {
   static constexpr int TK = 64;                    // keys per tile
@@ -1633,7 +1655,7 @@ cudaError_t launch_shared(ShArgs a, const uint16_t* k, const uint16_t* v, const 
   // The join: four warps a token while the (token, head) pairs do not fill the
   // SMs, else a warp.
   // The tokens that may have pieces: all, or those of sequences with few rows
-  // (one prompt of 8,192: 714 us with a grid over all of them, 669 over nine).
+  // (a prompt of 8,192: 714 us with a grid over all of them, 669 over nine).
   const long long most = (long long)a.batch * (a.few / a.gq);
   const int toks = a.own_joins && most < a.rows ? int(most) : a.rows;
   const int wpt = toks <= 256 && (long long)toks * a.nq <= 16LL * sms ? 4 : 1;
@@ -1690,9 +1712,9 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
   // sequences that fill their row tiles by themselves (512 packed rows each on
   // average), for which a tile with the prefix ahead of the own positions does
   // the same work and leaves no pieces to join.  Behind a long prefix such tiles
-  // are few and long, and two passes fill the last wave better (~1,150 tokens a
-  // sequence: 3 behind 4,000 positions 430 us with a pass of the prefix, 385
-  // without; 4 behind 8,192 702 and 735).
+  // are few and long, and two passes fill the last wave better (~1,000 tokens a
+  // sequence: 3 behind 4,000 positions 393 us with a pass of the prefix, 347
+  // without; 4 behind 8,192 658 and 692; 4 of ~520 behind 8, 45 and 34).
   const long long packed = (long long)rows * a.gq;
   a.with_prefix = P > 0 && ((long long)batch * P <= 4096 || (packed >= 512LL * batch && P <= 4096));
   a.prefix_few = P > 0 && !a.with_prefix && packed <= p.few;

@@ -374,10 +374,10 @@ W4A_API int w4a_paged_kv_layer(const W4AConfig* cfg, int n_pages, int page_size,
  *   max_rows are -1 in both.
  * All device int32: n_new, lens, lens_out [batch]; state, state_out [2];
  * queue [n_queue] and table [batch][table_width] updated in place; row_start
- * [batch + 1]; slots, pos [max_rows].  The outputs must not overlap the inputs
- * (lens_out and state_out are other buffers: a step that failed, or a graph
- * replay, can start again from the old ones); entries of table past a
- * sequence's pages are left as they are.
+ * [batch + 1]; slots, pos [max_rows], at most 2^30.  The outputs must not
+ * overlap the inputs (lens_out and state_out are other buffers: a step that
+ * failed, or a graph replay, can start again from the old ones); entries of
+ * table past a sequence's pages are left as they are.
  * All or nothing: when pages, table width or max_rows do not suffice, or an
  * input is out of range, nothing is taken or returned, lens_out = lens,
  * state_out = state, there are no rows, and w4a_check reports W4A_ERR_KERNEL.
@@ -399,7 +399,7 @@ W4A_API int w4a_paged_plan(const int32_t* n_new, const int32_t* lens, const int3
  * slot outside the cache, or a negative position, is skipped and reported by
  * w4a_check.  The angle is formed in fp64, so far positions keep their phase.
  * Of cfg n_heads, n_kv_heads, head_dim, eps and the rotation's fields are
- * used; (n_heads + 2 n_kv_heads) * head_dim <= 25,600.  qkv, q_out, the gains
+ * used; (n_heads + 2 n_kv_heads) * head_dim <= 25,600, rows <= 2^30.  qkv, q_out, the gains
  * and the pages 16-byte aligned.  ws as for w4a_paged_plan. */
 W4A_API int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, int64_t ld, int rows, const float* q_gain,
                       const float* k_gain, const int32_t* pos, const int32_t* slots, uint16_t* q_out,

@@ -349,6 +349,12 @@ def test_attention_with_rising_scores(api):
         assert np.all(np.abs(np64(out) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -9) * size)
 
 
+def test_the_widest_window_is_none(api):
+    for P, lens, new in ((2000, [300, 77], [1, 1]), (700, [500, 90], [300, 20]), (5000, [40, 700], [9, 8])):
+        c = attn_case(len(lens), 40, 8, 128, 64, P, lens, new)
+        assert torch.equal(run_attn(api, c, 2 ** 31 - 1), run_attn(api, c, 0))
+
+
 def test_attention_one_workspace_for_many_shapes(api):
     """A workspace of the largest call serves the others, in any order, twice."""
     cases = [attn_case(i, *ATTN[i][:7]) for i in (5, 8, 10, 12, 5)]

@@ -25,7 +25,7 @@ def plan_args(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(n_new=None), "ARG"), (dict(state=None), "ARG"), (dict(slots=None), "ARG"), (dict(ws=None), "ARG"),
     (dict(batch=0), "SHAPE"), (dict(batch=4097), "SHAPE"), (dict(width=0), "SHAPE"), (dict(prefix=-1), "SHAPE"),
-    (dict(max_rows=-1), "SHAPE"), (dict(page=8), "SHAPE"), (dict(page=48), "SHAPE"), (dict(page=512), "SHAPE"),
+    (dict(max_rows=-1), "SHAPE"), (dict(max_rows=(1 << 30) + 1), "SHAPE"), (dict(page=8), "SHAPE"), (dict(page=48), "SHAPE"), (dict(page=512), "SHAPE"),
     (dict(n_queue=0), "SHAPE"), (dict(n_queue=1 << 27, page=16), "SHAPE"), (dict(ws=P(0x9008)), "ALIGN"),
     (dict(ws_bytes=255), "WORKSPACE"),
     (dict(lens_out=P(0x2000)), "ARG"), (dict(state_out=P(0x3004)), "ARG"), (dict(slots=P(0x8000)), "ARG"),
@@ -46,7 +46,7 @@ def prep_args(c, **kw):
     (dict(cfg=None), "ARG"), (dict(qkv=None), "ARG"), (dict(k=None), "ARG"), (dict(rows=0), "SHAPE"),
     (dict(ld=764), "SHAPE"), (dict(ld=770), "SHAPE"), (dict(page=17), "SHAPE"), (dict(n_pages=0), "SHAPE"),
     (dict(qkv=P(0x1004)), "ALIGN"), (dict(q=P(0x1002)), "ALIGN"), (dict(v=P(0x1008)), "ALIGN"),
-    (dict(ws_bytes=0), "WORKSPACE")])
+    (dict(ws_bytes=0), "WORKSPACE"), (dict(rows=(1 << 30) + 1), "SHAPE")])
 def test_prep_refusals(lib, kw, code):
     assert lib.w4a_qk_prep_paged(*prep_args(config.tiny().to_c(), **kw)) == getattr(_abi, "ERR_" + code)
 

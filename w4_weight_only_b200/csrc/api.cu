@@ -1181,7 +1181,7 @@ int w4a_paged_plan(const int32_t* n_new, const int32_t* lens, const int32_t* sta
                    size_t ws_bytes, void* stream) {
   if (!n_new || !lens || !state || !queue || !table || !lens_out || !state_out || !row_start || !ws)
     return fail(W4A_ERR_ARG, "null pointer");
-  if (max_rows < 0) return fail(W4A_ERR_SHAPE, "max_rows %d", max_rows);
+  if (max_rows < 0 || max_rows > (1 << 30)) return fail(W4A_ERR_SHAPE, "max_rows %d (0..2^30)", max_rows);
   if (max_rows > 0 && (!slots || !pos)) return fail(W4A_ERR_ARG, "null pointer");
   if (batch < 1 || batch > MAX_PAGED_BATCH) return fail(W4A_ERR_SHAPE, "batch %d (1..%d)", batch, MAX_PAGED_BATCH);
   if (table_width < 1 || prefix_len < 0) return fail(W4A_ERR_SHAPE, "table_width %d prefix_len %d", table_width, prefix_len);
@@ -1225,7 +1225,7 @@ int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, int64_t 
   if (rc) return rc;
   const int width = (nq + 2 * nkv) * hd;
   if (width > 25600) return fail(W4A_ERR_SHAPE, "a QKV row of %d values (at most 25600)", width);
-  if (rows < 1) return fail(W4A_ERR_SHAPE, "rows %d", rows);
+  if (rows < 1 || rows > (1 << 30)) return fail(W4A_ERR_SHAPE, "rows %d (1..2^30)", rows);
   if (ld < width || ld % 4) return fail(W4A_ERR_SHAPE, "row stride %lld (at least %d, a multiple of 4)", (long long)ld, width);
   if (!aligned16(qkv) || !aligned16(q_gain) || !aligned16(k_gain) || !aligned16(q_out) || !aligned16(k_pages) ||
       !aligned16(v_pages) || !aligned16(ws))

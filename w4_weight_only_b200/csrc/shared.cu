@@ -1741,7 +1741,7 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
     if (!p.many && p.few == 16) {
       const double unit = 0.97 * (2.0 * p.pairs + (p.rest_alt ? 1.0 : 2.0) * p.rest) * tiles(P);
       double keys = double(width) * page;
-      if (window > 0 && keys > window + max_new) keys = window + max_new;
+      if (window > 0 && keys > double(window) + max_new) keys = double(window) + max_new;
       const double own_bytes = batch * keys * nkv * hd * 4.0, rate = 85e3;
       auto prefix_us = [&](int n) { return 12.0 + unit / n; };
       auto own_us = [&](int n) { return own_bytes / (n * rate < 6.5e6 ? n * rate : 6.5e6); };

@@ -1733,16 +1733,17 @@ cudaError_t launch_attn_shared(const uint16_t* q, int rows, int batch, int nq, i
     // cores, few_kernel by memory, which half of the SMs keep busy.  The split
     // is the one with the shortest longer side, by what was measured: 12 us
     // and 0.97 us a key tile of 128 rows for the prefix; 85 GB/s an SM, 6.5 TB/s
-    // in all, for the keys that the tables have room for (the lengths are on the
-    // device).  One after the
-    // other unless that is a tenth slower.  (16 sequences behind 8,192
-    // positions: 49 us one after the other, 36 side by side.)
+    // in all, for 85 % of the keys that the tables have room for (the lengths are
+    // on the device, and tables are seldom full).  One after the other unless
+    // that is a tenth slower.  (16 sequences behind 8,192 positions: 49 us one
+    // after the other, 35 side by side.  100 of up to 1,000 behind 8,192: 103 us
+    // with the prefix on the 40 SMs that full tables would leave it, 72 on 48.)
     int budget = sms;
     if (!p.many && p.few == 16) {
       const double unit = 0.97 * (2.0 * p.pairs + (p.rest_alt ? 1.0 : 2.0) * p.rest) * tiles(P);
       double keys = double(width) * page;
       if (window > 0 && keys > double(window) + max_new) keys = double(window) + max_new;
-      const double own_bytes = batch * keys * nkv * hd * 4.0, rate = 85e3;
+      const double own_bytes = 0.85 * batch * keys * nkv * hd * 4.0, rate = 85e3;
       auto prefix_us = [&](int n) { return 12.0 + unit / n; };
       auto own_us = [&](int n) { return own_bytes / (n * rate < 6.5e6 ? n * rate : 6.5e6); };
       double best = 0.9 * (prefix_us(sms) + own_us(sms));

@@ -28,10 +28,11 @@
 // Measured, 40 query heads over 8 of K / V, head_dim 128, GPU time of a call in
 // a full queue (a call that finds the queue empty takes the host's 12 to 16 us
 // at least):
-//   a prompt of 8,192: 636 us, 1,080 TFLOP/s (softmax and tensor core in turn)
+//   a prompt of 8,192: 636 us, 1,080 TFLOP/s; call after call for seconds 715 us,
+//     at 1,735 MHz under the power cap
 //   3,722 rows of 4 sequences behind 8,192 positions: 658 us, 1,050 TFLOP/s
 //   16 sequences of one row, up to 16,384 own positions: 97 us, 6.2 TB/s
-//   16 of one row and up to 2,048 behind 8,192: 36 us
+//   16 of one row and up to 2,048 behind 8,192: 35 us
 //   64 of one row and up to 1,024 behind 32,768: 102 us, 430 TFLOP/s
 //   24 of 5 to 9 rows and up to 1,500 behind 4,097, pages of 16: 86 us
 #include <cuda.h>

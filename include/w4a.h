@@ -423,8 +423,10 @@ W4A_API int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, 
  * prefix_table may be NULL when
  * prefix_len is 0.  Positions that no row of the call sees (the unwritten rest
  * of a page, keys before every window) never reach an output, whatever the
- * pages hold there; an infinity or NaN at a position that some row sees can
- * reach the other rows of the call too.
+ * pages hold there.  A NaN or an infinity among what a row sees gives what the
+ * formula gives: a NaN or +inf score makes the (row, head) NaN, a score of -inf
+ * takes its key out (all of them: NaN); a V that is not finite makes its column
+ * not finite, and can reach that column of the other rows of the call too.
  * A sequence whose numbers do not fit (n > max_new, n > lens[b], lens[b] beyond
  * the table, rows outside [0, rows]) is skipped, a page id outside the cache
  * makes the outputs that read it meaningless; both are reported by w4a_check.

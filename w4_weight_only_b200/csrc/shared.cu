@@ -10,7 +10,12 @@
 // A softmax over a union of key ranges is the join of the softmaxes over the
 // ranges: each piece keeps a reference m (log2 units), l = sum 2^(s - m) and
 // O = sum 2^(s - m) v in fp32, and pieces join as sum O 2^(m - M) /
-// sum l 2^(m - M).  So the work is cut twice: a long prefix apart from the own
+// sum l 2^(m - M).  A piece that held none of a row's keys has l = 0 (its O may
+// be unwritten) and is left out; every other one counts, so that a NaN or an
+// infinity among what a row sees reaches its output whatever the cut: a piece
+// with keys has l >= 1, a NaN, or l = 0 where all its scores are -inf.  A row
+// sees itself at least, so l = 0 in the end means that every score was -inf, and
+// 1 / l makes that the NaN of the formula.  So the work is cut twice: a long prefix apart from the own
 // positions, because all rows share its keys (a short one is read ahead of
 // each sequence's own, see with_prefix), and both along the keys, to fill the
 // SMs when there are few rows.
@@ -733,13 +738,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 #pragma unroll 1
           for (int i = 0; i < np; ++i) {
             const float2 ml = a.ml_part[i * stride + line];
-            if (!(ml.y > 0.f)) continue;
+            if (ml.y == 0.f) continue;
             const float M = fmaxf(m_run, ml.x);
             L = L * exp2f(m_run - M) + ml.y * exp2f(ml.x - M);
             m_run = M;
           }
         }
-        const float inv = L > 0.f ? 1.f / L : 0.f;
+        const float inv = 1.f / L;
         const float f = live ? exp2f(m0 - m_run) * inv : 0.f;
         f0 *= f;
         f1 *= f;
@@ -777,7 +782,7 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
             }
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-              if (!(ml[u].y > 0.f)) continue;  // an empty piece's O was not written
+              if (ml[u].y == 0.f) continue;  // an empty piece's O was not written
               const float f = exp2f(ml[u].x - w[u].x) * w[u].y;
               x[u] = make_float4(fmaf(y[u].x, f, x[u].x), fmaf(y[u].y, f, x[u].y), fmaf(y[u].z, f, x[u].z),
                                  fmaf(y[u].w, f, x[u].w));
@@ -1269,7 +1274,7 @@ __global__ void __launch_bounds__(Fw<HD, MG>::THREADS, Fw<HD, MG>::PER_SM)
           if (!ok) continue;
           const size_t line = size_t(s_line[pr]);
           if (whole) {
-            const float inv = L > 0.f ? 1.f / L : 0.f;
+            const float inv = 1.f / L;
             *reinterpret_cast<uint2*>(a.out + line * HD + c4 * 4) =
                 make_uint2(cvt_bf16x2(y.x * inv, y.y * inv), cvt_bf16x2(y.z * inv, y.w * inv));
           } else {
@@ -1420,7 +1425,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
                              : (size_t)((mine ? c0 + i - in_slots : p0 + i - in_slots - nc) * a.few + (mine ? crow : prow));
       const float2 ml = (slot ? a.ml_part : a.ml_cont)[at];
       const float* src = (slot ? a.o_part : a.o_cont) + at * HD;
-      const bool there = i1 < total && ml.y > 0.f;
+      const bool there = i1 < total && ml.y != 0.f;
       float m = there ? ml.x : -INFINITY;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -1431,15 +1436,15 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] *= f;
       }
-      const float w = there ? exp2f(ml.x - M) : 0.f;
-      L = fmaf(there ? ml.y : 0.f, w, L);  // this lane's share; summed below
+      const float w = there ? exp2f(ml.x - M) : -1.f;  // (-1: nothing there; a weight may be 0 or NaN)
+      if (there) L = fmaf(ml.y, w, L);  // this lane's share; summed below
       const int n32 = min(32, (total - i0 - share + wpt - 1) / wpt);
 #pragma unroll 1
       for (int k0 = 0; k0 < n32; k0 += JCH) {
         float x[JCH][E];
 #pragma unroll
         for (int k = 0; k < JCH; ++k) {
-          // (an index past the last piece is read as that piece, with weight 0)
+          // (an index past the last piece is read as that piece, with weight -1)
           const float* s_k = reinterpret_cast<const float*>(
               __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k0 + k)) + lane * E;
           if (E == 4)
@@ -1452,7 +1457,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
           const float f = __shfl_sync(0xffffffffu, w, k0 + k);
           // an empty piece's O was not written
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(f != 0.f ? x[k][e] : 0.f, f, acc[e]);
+          for (int e = 0; e < E; ++e) acc[e] = f < 0.f ? acc[e] : fmaf(x[k][e], f, acc[e]);
         }
       }
     }
@@ -1464,7 +1469,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
       for (int e = 0; e < E; ++e) s_acc[warp][lane * E + e] = acc[e];
       if (lane == 0) s_ml[warp] = make_float2(M, L);
     } else {
-      const float inv = L > 0.f ? 1.f / L : 0.f;
+      const float inv = 1.f / L;
       uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + line * HD + lane * E);
 #pragma unroll
       for (int e = 0; e < E; e += 2) dst[e / 2] = cvt_bf16x2(acc[e] * inv, acc[e + 1] * inv);
@@ -1487,7 +1492,7 @@ __global__ void __launch_bounds__(JT) join_kernel(const __grid_constant__ ShArgs
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = fmaf(s_acc[w0 + w][lane * E + e], f, acc[e]);
     }
-    const float inv = L > 0.f ? 1.f / L : 0.f;
+    const float inv = 1.f / L;
     uint32_t* dst = reinterpret_cast<uint32_t*>(a.out + ((size_t)tok * a.nq + head) * HD + lane * E);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = cvt_bf16x2(acc[e] * inv, acc[e + 1] * inv);

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <mutex>
 
 #include "../../include/w4a.h"
 
@@ -172,20 +173,26 @@ struct EngineParams {
   int trace_phases;
 };
 
-// Allows a kernel `bytes` of dynamic shared memory; remembered per kernel and
-// device (mark: one per kernel), since the runtime call costs as much as a
-// launch.  Host threads may race to the same result.
+// Allows a kernel at least `bytes` of dynamic shared memory; what it has is
+// remembered per kernel and device (mark: one per kernel), since the runtime call
+// costs as much as a launch.  The size may change from call to call: the limit
+// is set and noted under one lock and never lowered, so that a note is never
+// above the kernel's limit, whichever host threads come at once.
 struct SmemMark {
   std::atomic<int> bytes[64] = {};
+  std::mutex mu;
 };
 inline cudaError_t allow_smem(const void* fn, int bytes, SmemMark& mark) {
   if (bytes <= 40 * 1024) return cudaSuccess;  // static and dynamic together fit the default 48 KB
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev < 64 && mark.bytes[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (mark.bytes[dev].load(std::memory_order_acquire) >= bytes) return cudaSuccess;
+  std::lock_guard<std::mutex> lk(mark.mu);
+  if (mark.bytes[dev].load(std::memory_order_relaxed) >= bytes) return cudaSuccess;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e == cudaSuccess && dev < 64) mark.bytes[dev].store(bytes, std::memory_order_relaxed);
+  if (e == cudaSuccess) mark.bytes[dev].store(bytes, std::memory_order_release);
   return e;
 }
 

@@ -1284,7 +1284,8 @@ int w4a_attn_shared(const uint16_t* q, int rows, int batch, int n_heads, int n_k
   if (rc) return rc;
   rc = check_pages(n_pages, page_size, n_kv_heads);
   if (rc) return rc;
-  if (prefix_len < 0 || prefix_len > (1 << 30)) return fail(W4A_ERR_SHAPE, "prefix_len %d (0..2^30)", prefix_len);
+  if (prefix_len < 0 || prefix_len >= (1 << 30))
+    return fail(W4A_ERR_SHAPE, "prefix_len %d (fewer than 2^30 positions)", prefix_len);
   if (prefix_len > 0 && !prefix_table) return fail(W4A_ERR_ARG, "null prefix_table");
   if (window < 0) return fail(W4A_ERR_SHAPE, "window %d", window);
   if (table_width < 1 || (long long)table_width * page_size >= (1LL << 30))

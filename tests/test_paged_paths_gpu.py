@@ -1,0 +1,98 @@
+"""Attention behind a shared prefix against the float64 oracle, one case or
+more for each way in which the host cuts a call (paged_paths.PATHS), and at the
+sizes of prompts and turns.
+
+Tolerance: as in test_paged_gpu.py (one rounding of the result, one of each
+weight, the scores'), and the sums in fp32: N visible keys add at most N 2^-24
+of sum p |v| in the numerator and as much in the sum of the weights.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as op
+from helpers import np64
+from paged_paths import PATHS
+from test_paged_gpu import api, attn_case, i32, run_attn  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def sampled(c, most):
+    """At most about `most` rows: the first and last of each sequence and those
+    around the borders of row tiles, then a spread of the others."""
+    n, g = c["start"][-1], c["q"].shape[1] // c["k"].shape[1]
+    if n <= most:
+        return list(range(n))
+    keep = {r for s in c["start"] for r in (s - 1, s)}
+    keep |= {x * 256 // g + d for x in (1, 2, 3, n * g // 256) for d in (-1, 0, 1)}
+    keep = sorted(r for r in keep if 0 <= r < n)
+    if len(keep) > most:
+        keep = keep[:: -(-len(keep) // most)]
+    return sorted(set(keep) | set(range(0, n, -(-n // max(1, most - len(keep))))))
+
+
+def close_rows(c, out, window, rows):
+    """Those rows against the oracle, each as a sequence of one row."""
+    lens, table = [], []
+    for r in rows:
+        b = max(s for s in range(len(c["lens"])) if c["start"][s] <= r < c["start"][s + 1])
+        lens.append(c["lens"][b] - (c["start"][b + 1] - 1 - r))
+        table.append(c["table"][b])
+    ref, size = op.attend(np64(c["q"][rows]), np64(c["k"]), np64(c["v"]), list(range(len(rows) + 1)), lens, table,
+                          c["ptab"], c["P"], window)
+    n = np.array([c["P"] + x if not window else min(window, c["P"] + x) for x in lens])[:, None, None]
+    err = np.abs(np64(out[rows]) - ref) - (2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -11 + 2 * n * 2.0 ** -24) * size)
+    assert np.all(err <= 0), (np.unravel_index(np.nanargmax(err), err.shape), np.nanmax(err))
+
+
+@pytest.mark.parametrize("name", PATHS)
+def test_path(api, name):
+    """Rows of pages that nothing sees hold NaN."""
+    (nq, nkv, hd, page, P, lens, new, window), pad, _ = PATHS[name]
+    c = attn_case(len(name), nq, nkv, hd, page, P, lens, new, pad=pad, junk=float("nan"))
+    n, out = c["start"][-1], torch.full_like(c["q"], 9.0)
+    run_attn(api, c, window, out=out)
+    assert torch.isfinite(out).all() and torch.all(out[n:] == 9.0)
+    close_rows(c, out, window, sampled(c, 60))
+    again = run_attn(api, c, window, out=torch.empty_like(out))
+    assert torch.equal(again[:n], out[:n])
+
+
+@pytest.mark.parametrize("P,new,more,window", [
+    (8192, [1300, 743, 855, 824], 200, 0), (8192, [1300, 743, 855, 824], 200, 4096), (1000, [1300, 700, 900], 0, 0),
+    (0, [4000], 0, 0), (0, [8192], 0, 0), (0, [8192], 0, 4096), (4097, [9, 7, 8, 5] * 6, 900, 0),
+    (4097, [9, 7, 8, 5] * 6, 900, 2000), (32768, [1] * 64, 900, 0), (6001, [1] * 16, 5900, 4096)])
+def test_sizes_of_use(api, P, new, more, window):
+    """Prompts, turns, drafts and decodes of the 32B shape: up to 40 rows of each."""
+    c = attn_case(len(new) + window, 40, 8, 128, 64, P, [n + (more * (i + 1)) // len(new) for i, n in enumerate(new)], new)
+    out = run_attn(api, c, window)
+    assert torch.isfinite(out).all()
+    close_rows(c, out, window, sampled(c, 40 if P < 32768 else 12))
+
+
+@pytest.mark.parametrize("P,lens,new", [
+    (5000, [201, 100, 300], [1, 1, 1]), (3000, [150] * 64, [1] * 64), (4500, [200] * 4, [100] * 4),
+    (4500, [300, 200], [40, 9])])
+def test_rising_scores_over_a_prefix_of_its_own(api, P, lens, new):
+    """Scores that grow along the keys to 2^100 of the first one's weight, over
+    a prefix that has pieces of its own: references differ between the pieces
+    as far as within them.  sum|q k| stays below 2^10, as in the test beside
+    the shorter prefixes; weights off by less than 2^-9 of themselves."""
+    c = attn_case(len(new), 40, 8, 128, 32, P, lens, new)
+    c["q"] = c["q"] * 0 + 1
+    flat = lambda x: x.transpose(1, 2).reshape(-1, 8, 128)
+    k = flat(c["k"]).clone()
+    top = P + max(lens)
+    for ids, n, base in [(c["ptab"], P, 0)] + [(c["table"][b], m, P) for b, m in enumerate(lens)]:
+        i = torch.arange(n, device="cuda")
+        at = i32(ids).long()[i // 32] * 32 + i % 32
+        k[at] = (k[at].float() * 0.1 + (3.4 * (i + base) / top * (1 + (i % 7 == 0)))[:, None, None]).to(torch.bfloat16)
+    c["k"] = k.view(-1, 32, 8, 128).transpose(1, 2).contiguous()
+    out = run_attn(api, c)
+    rows = sampled(c, 40)
+    one = [(c["table"][b], m - (c["start"][b + 1] - 1 - r)) for r in rows for b, m in enumerate(lens)
+           if c["start"][b] <= r < c["start"][b + 1]]
+    ref, size = op.attend(np64(c["q"][rows]), np64(c["k"]), np64(c["v"]), list(range(len(rows) + 1)),
+                          [m for _, m in one], [t for t, _ in one], c["ptab"], P, 0)
+    assert np.all(np.abs(np64(out[rows]) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -9) * size)

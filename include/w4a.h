@@ -352,7 +352,9 @@ W4A_API int w4a_attn_prefill(const uint16_t* q, const uint16_t* k_cache, const u
  * row is then the prefix table of the others.
  * One step is w4a_paged_plan, then for every layer w4a_qk_prep_paged and
  * w4a_attn_shared, on one stream; nothing is read back by the host, so a step
- * can be captured into a CUDA graph. */
+ * can be captured into a CUDA graph.  A step without rows (it only ends
+ * sequences) is the plan alone: the other two take at least one row, which may
+ * be a row of padding. */
 W4A_API int w4a_paged_kv_bytes(const W4AConfig* cfg, int n_pages, int page_size, size_t* bytes);
 /* Byte offsets of layer l's K and V pages. */
 W4A_API int w4a_paged_kv_layer(const W4AConfig* cfg, int n_pages, int page_size, int layer, size_t* k_offset,

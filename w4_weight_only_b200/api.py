@@ -594,8 +594,8 @@ def qk_prep_paged(cfg: Config, full: bool, qkv: torch.Tensor, q_gain: torch.Tens
                   ws: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """QK-norm, rotation and append of a step's rows (w4a_qk_prep_paged): qkv
     fp32 [rows, q_dim + 2 kv_dim] (rows may be strided), pos and slots int32
-    [rows] from paged_plan (rows with slot -1 are skipped); returns q bf16
-    [rows, n_heads, hd]."""
+    [rows] from paged_plan (rows with slot -1 are skipped; no rows: nothing to
+    do); returns q bf16 [rows, n_heads, hd]."""
     nq, nkv, hd, dev, f32, bf16 = cfg.n_heads, cfg.n_kv_heads, cfg.head_dim, qkv.device, torch.float32, torch.bfloat16
     if qkv.dtype != f32:
         raise TypeError(f"qkv: expected {f32}, got {qkv.dtype}")
@@ -616,18 +616,21 @@ def qk_prep_paged(cfg: Config, full: bool, qkv: torch.Tensor, q_gain: torch.Tens
     c = _abi.W4AConfig(n_heads=nq, n_kv_heads=nkv, head_dim=hd, rope_theta=cfg.rope_theta, yarn_factor=cfg.yarn_factor,
                        yarn_orig_ctx=cfg.yarn_orig_ctx, yarn_beta_fast=cfg.yarn_beta_fast,
                        yarn_beta_slow=cfg.yarn_beta_slow, eps=cfg.eps)
-    _call_on(dev, "w4a_qk_prep_paged", C.byref(c), 1 if full else 0, qkv.data_ptr(), ld, R,
-             _ptr(q_gain, f32, "q_gain", (nq * hd,), dev), _ptr(k_gain, f32, "k_gain", (nkv * hd,), dev),
-             _ptr(pos, torch.int32, "pos", (R,), dev), _ptr(slots, torch.int32, "slots", (R,), dev),
-             _ptr(q_out, bf16, "q_out", (R, nq, hd), dev), _ptr(k_pages, bf16, "k_pages", (n_pages, nkv, page, hd), dev),
-             _ptr(v_pages, bf16, "v_pages", (n_pages, nkv, page, hd), dev), n_pages, page,
-             _ptr(ws, torch.uint8, "ws", ws.shape, dev), ws.numel())
+    args = (qkv.data_ptr(), ld, R, _ptr(q_gain, f32, "q_gain", (nq * hd,), dev),
+            _ptr(k_gain, f32, "k_gain", (nkv * hd,), dev), _ptr(pos, torch.int32, "pos", (R,), dev),
+            _ptr(slots, torch.int32, "slots", (R,), dev), _ptr(q_out, bf16, "q_out", (R, nq, hd), dev),
+            _ptr(k_pages, bf16, "k_pages", (n_pages, nkv, page, hd), dev),
+            _ptr(v_pages, bf16, "v_pages", (n_pages, nkv, page, hd), dev), n_pages, page,
+            _ptr(ws, torch.uint8, "ws", ws.shape, dev), ws.numel())
+    if R > 0:  # (a step that only ends sequences has no rows)
+        _call_on(dev, "w4a_qk_prep_paged", C.byref(c), 1 if full else 0, *args)
     return q_out
 
 
 def attn_shared_workspace(rows: int, batch: int, n_heads: int, n_kv_heads: int, head_dim: int, max_new: int = 1,
                           device=None) -> torch.Tensor:
-    return zeros_workspace(_size_out("w4a_attn_shared_workspace_bytes", rows, batch, n_heads, n_kv_heads, head_dim,
+    """Scratch of attn_shared calls of these sizes (no rows count as one)."""
+    return zeros_workspace(_size_out("w4a_attn_shared_workspace_bytes", max(rows, 1), batch, n_heads, n_kv_heads, head_dim,
                                      max_new), device)
 
 
@@ -640,7 +643,8 @@ def attn_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, r
     and lens [B] from paged_plan, table [B, width]; the first prefix_len
     positions of every sequence in the pages prefix_table, a long prefix read
     once for the batch.  max_new: the most rows a sequence has.  Returns bf16 [rows,
-    n_heads, hd]; rows behind the last sequence are left as they were."""
+    n_heads, hd]; rows behind the last sequence are left as they were.  No rows
+    (a step that only ends sequences): nothing to do."""
     if q.dim() != 3 or k_pages.dim() != 4 or table.dim() != 2:
         raise ValueError(f"expected q [rows, n_heads, hd], k_pages [n_pages, n_kv, page_size, hd] and table [batch, "
                          f"width], got {list(q.shape)}, {list(k_pages.shape)} and {list(table.shape)}")
@@ -656,12 +660,14 @@ def attn_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, r
         ws = attn_shared_workspace(R, B, nq, nkv, hd, max_new, dev)
     if out is None:
         out = torch.empty_like(q)
-    _call_on(dev, "w4a_attn_shared", _ptr(q, bf16, "q", (R, nq, hd), dev), R, B, nq, nkv, hd,
-             _ptr(k_pages, bf16, "k_pages", (n_pages, nkv, page, hd), dev),
-             _ptr(v_pages, bf16, "v_pages", (n_pages, nkv, page, hd), dev), n_pages, page,
-             _ptr(row_start, i32, "row_start", (B + 1,), dev), _ptr(lens, i32, "lens", (B,), dev),
-             _ptr(table, i32, "table", (B, table.shape[1]), dev), table.shape[1], prefix, prefix_len, window, max_new,
-             _ptr(out, bf16, "out", (R, nq, hd), dev), _ptr(ws, torch.uint8, "ws", ws.shape, dev), ws.numel())
+    args = (_ptr(q, bf16, "q", (R, nq, hd), dev), R, B, nq, nkv, hd,
+            _ptr(k_pages, bf16, "k_pages", (n_pages, nkv, page, hd), dev),
+            _ptr(v_pages, bf16, "v_pages", (n_pages, nkv, page, hd), dev), n_pages, page,
+            _ptr(row_start, i32, "row_start", (B + 1,), dev), _ptr(lens, i32, "lens", (B,), dev),
+            _ptr(table, i32, "table", (B, table.shape[1]), dev), table.shape[1], prefix, prefix_len, window, max_new,
+            _ptr(out, bf16, "out", (R, nq, hd), dev), _ptr(ws, torch.uint8, "ws", ws.shape, dev), ws.numel())
+    if R > 0:
+        _call_on(dev, "w4a_attn_shared", *args)
     return out
 
 

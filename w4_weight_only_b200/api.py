@@ -553,14 +553,19 @@ class PagedKVCache:
                 torch.tensor([0, self.n_pages], dtype=torch.int32, device=dev))
 
 
-class PagedPlan(NamedTuple):
-    """What w4a_paged_plan writes: the sequences' new own lengths [B], the free
-    queue's state [2], row_start [B + 1], slots and positions [max_rows]."""
+class _PlanTensors(NamedTuple):
     lens: torch.Tensor
     state: torch.Tensor
     row_start: torch.Tensor
     slots: torch.Tensor
     pos: torch.Tensor
+
+
+class PagedPlan(_PlanTensors):
+    """What w4a_paged_plan writes: the sequences' new own lengths [B], the free
+    queue's state [2], row_start [B + 1], slots and positions [max_rows].  ws:
+    the workspace that holds the call's error word (check(plan.ws))."""
+    ws: Optional[torch.Tensor] = None
 
 
 def paged_plan(n_new: torch.Tensor, lens: torch.Tensor, state: torch.Tensor, queue: torch.Tensor, table: torch.Tensor,
@@ -569,8 +574,10 @@ def paged_plan(n_new: torch.Tensor, lens: torch.Tensor, state: torch.Tensor, que
     """Block tables and slot maps of one step (w4a_paged_plan): n_new int32 [B]
     new tokens of each sequence (-1 ends it), lens [B] own positions so far,
     the free queue [n_pages] with its state {head, count}; queue and table
-    [B, width] are updated in place.  check(ws) raises if pages, table width or
-    rows did not suffice (nothing has changed then)."""
+    [B, width] are updated in place.  check(plan.ws) raises if pages, table width
+    or rows did not suffice (nothing has changed then, and the step has no
+    rows).  ws: 256 bytes or any larger workspace of the step's (zeros_workspace,
+    attn_shared_workspace); by default one of this call's own."""
     B, N, dev, i32 = n_new.numel(), queue.numel(), n_new.device, torch.int32
     if table.dim() != 2:
         raise ValueError(f"table: expected [batch, width], got {list(table.shape)}")
@@ -586,6 +593,9 @@ def paged_plan(n_new: torch.Tensor, lens: torch.Tensor, state: torch.Tensor, que
     if ws is None:
         ws = zeros_workspace(256, dev)
     _call_on(dev, "w4a_paged_plan", *ins, *outs, max_rows, _ptr(ws, torch.uint8, "ws", ws.shape, dev), ws.numel())
+    if not isinstance(out, PagedPlan):
+        out = PagedPlan(*out)
+    out.ws = ws
     return out
 
 
@@ -595,7 +605,10 @@ def qk_prep_paged(cfg: Config, full: bool, qkv: torch.Tensor, q_gain: torch.Tens
     """QK-norm, rotation and append of a step's rows (w4a_qk_prep_paged): qkv
     fp32 [rows, q_dim + 2 kv_dim] (rows may be strided), pos and slots int32
     [rows] from paged_plan (rows with slot -1 are skipped; no rows: nothing to
-    do); returns q bf16 [rows, n_heads, hd]."""
+    do); returns q bf16 [rows, n_heads, hd].  Pass ws (plan.ws, or any workspace
+    of the step's) and check(ws) to learn of slots outside the cache: without one
+    the error word goes with the call, and a skipped row of a q that the call
+    allocates is uninitialised."""
     nq, nkv, hd, dev, f32, bf16 = cfg.n_heads, cfg.n_kv_heads, cfg.head_dim, qkv.device, torch.float32, torch.bfloat16
     if qkv.dtype != f32:
         raise TypeError(f"qkv: expected {f32}, got {qkv.dtype}")
@@ -629,9 +642,12 @@ def qk_prep_paged(cfg: Config, full: bool, qkv: torch.Tensor, q_gain: torch.Tens
 
 def attn_shared_workspace(rows: int, batch: int, n_heads: int, n_kv_heads: int, head_dim: int, max_new: int = 1,
                           device=None) -> torch.Tensor:
-    """Scratch of attn_shared calls of these sizes (no rows count as one)."""
-    return zeros_workspace(_size_out("w4a_attn_shared_workspace_bytes", max(rows, 1), batch, n_heads, n_kv_heads, head_dim,
-                                     max_new), device)
+    """Scratch of attn_shared calls of these sizes (no rows count as one); its
+    first 256 bytes, the error word, are zero."""
+    ws = torch.empty(_size_out("w4a_attn_shared_workspace_bytes", max(rows, 1), batch, n_heads, n_kv_heads, head_dim,
+                               max_new), dtype=torch.uint8, device=device or "cuda")
+    ws[:256].zero_()
+    return ws
 
 
 def attn_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, row_start: torch.Tensor,
@@ -643,8 +659,11 @@ def attn_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, r
     and lens [B] from paged_plan, table [B, width]; the first prefix_len
     positions of every sequence in the pages prefix_table, a long prefix read
     once for the batch.  max_new: the most rows a sequence has.  Returns bf16 [rows,
-    n_heads, hd]; rows behind the last sequence are left as they were.  No rows
-    (a step that only ends sequences): nothing to do."""
+    n_heads, hd]; rows behind the last sequence are left as they were (of
+    an output that the call allocates: uninitialised).  No rows (a step that only
+    ends sequences): nothing to do.  Pass ws (attn_shared_workspace, made once;
+    the step's other calls may have it too) and check(ws) to learn of sequences
+    that were skipped: without one the error word goes with the call."""
     if q.dim() != 3 or k_pages.dim() != 4 or table.dim() != 2:
         raise ValueError(f"expected q [rows, n_heads, hd], k_pages [n_pages, n_kv, page_size, hd] and table [batch, "
                          f"width], got {list(q.shape)}, {list(k_pages.shape)} and {list(table.shape)}")

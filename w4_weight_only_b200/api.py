@@ -691,8 +691,9 @@ def attn_shared(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, r
 
 
 def check(ws: torch.Tensor):
-    """Synchronise and raise if the workspace's device error word is set."""
-    call("w4a_check", _p(ws), ws.numel(), _stream())
+    """Synchronise with the current stream of the workspace's device and raise
+    if the workspace's device error word is set."""
+    _call_on(ws.device, "w4a_check", _p(ws), ws.numel())
 
 
 def check_noalloc():

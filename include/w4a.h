@@ -402,7 +402,8 @@ W4A_API int w4a_paged_plan(const int32_t* n_new, const int32_t* lens, const int3
  * w4a_check.  The angle is formed in fp64, so far positions keep their phase.
  * Of cfg n_heads, n_kv_heads, head_dim, eps and the rotation's fields are
  * used; (n_heads + 2 n_kv_heads) * head_dim <= 25,600, rows <= 2^30.  qkv, q_out, the gains
- * and the pages 16-byte aligned.  ws as for w4a_paged_plan. */
+ * and the pages 16-byte aligned; q_out, k_pages and v_pages on no input and not
+ * on one another.  ws as for w4a_paged_plan. */
 W4A_API int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, int64_t ld, int rows, const float* q_gain,
                       const float* k_gain, const int32_t* pos, const int32_t* slots, uint16_t* q_out,
                       uint16_t* k_pages, uint16_t* v_pages, int n_pages, int page_size, void* ws, size_t ws_bytes,

@@ -1151,6 +1151,22 @@ static bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return an && bn && x < y + bn && y < x + an;
 }
 
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// No output on an input or on another output.
+static int check_apart(const Range* in, int n_in, const Range* out, int n_out) {
+  for (int o = 0; o < n_out; ++o) {
+    for (int i = 0; i < n_in; ++i)
+      if (overlap(in[i].p, in[i].n, out[o].p, out[o].n)) return fail(W4A_ERR_ARG, "an output overlaps an input");
+    for (int i = 0; i < o; ++i)
+      if (overlap(out[i].p, out[i].n, out[o].p, out[o].n)) return fail(W4A_ERR_ARG, "two outputs overlap");
+  }
+  return W4A_OK;
+}
+
 int w4a_paged_kv_bytes(const W4AConfig* cfg, int n_pages, int page_size, size_t* bytes) {
   int rc = check_config(cfg);
   if (rc) return rc;
@@ -1187,23 +1203,16 @@ int w4a_paged_plan(const int32_t* n_new, const int32_t* lens, const int32_t* sta
   if (table_width < 1 || prefix_len < 0) return fail(W4A_ERR_SHAPE, "table_width %d prefix_len %d", table_width, prefix_len);
   int rc = check_pages(n_queue, page_size, 1);
   if (rc) return rc;
-  const struct {
-    const void* p;
-    size_t n;
-  } in[3] = {{n_new, (size_t)batch * 4}, {lens, (size_t)batch * 4}, {state, 8}},
-    out[7] = {{queue, (size_t)n_queue * 4},
-              {table, (size_t)batch * table_width * 4},
-              {lens_out, (size_t)batch * 4},
-              {state_out, 8},
-              {row_start, (size_t)(batch + 1) * 4},
-              {slots, (size_t)max_rows * 4},
-              {pos, (size_t)max_rows * 4}};
-  for (int o = 0; o < 7; ++o) {
-    for (int i = 0; i < 3; ++i)
-      if (overlap(in[i].p, in[i].n, out[o].p, out[o].n)) return fail(W4A_ERR_ARG, "an output overlaps an input");
-    for (int i = 0; i < o; ++i)
-      if (overlap(out[i].p, out[i].n, out[o].p, out[o].n)) return fail(W4A_ERR_ARG, "two outputs overlap");
-  }
+  const Range in[3] = {{n_new, (size_t)batch * 4}, {lens, (size_t)batch * 4}, {state, 8}},
+              out[7] = {{queue, (size_t)n_queue * 4},
+                        {table, (size_t)batch * table_width * 4},
+                        {lens_out, (size_t)batch * 4},
+                        {state_out, 8},
+                        {row_start, (size_t)(batch + 1) * 4},
+                        {slots, (size_t)max_rows * 4},
+                        {pos, (size_t)max_rows * 4}};
+  rc = check_apart(in, 3, out, 7);
+  if (rc) return rc;
   if (!aligned16(ws)) return fail(W4A_ERR_ALIGN, "workspace not 16-byte aligned");
   if (ws_bytes < 256) return fail(W4A_ERR_WORKSPACE, "workspace %zu < 256 bytes", ws_bytes);
   CK(launch_paged_plan(n_new, lens, state, queue, table, lens_out, state_out, row_start, slots, pos,
@@ -1231,6 +1240,15 @@ int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, int64_t 
       !aligned16(v_pages) || !aligned16(ws))
     return fail(W4A_ERR_ALIGN, "misaligned pointer");
   if (ws_bytes < 256) return fail(W4A_ERR_WORKSPACE, "workspace %zu < 256 bytes", ws_bytes);
+  const size_t pages = (size_t)n_pages * nkv * page_size * hd * 2;
+  const Range in[5] = {{qkv, ((size_t)(rows - 1) * ld + width) * 4},
+                       {q_gain, (size_t)nq * hd * 4},
+                       {k_gain, (size_t)nkv * hd * 4},
+                       {pos, (size_t)rows * 4},
+                       {slots, (size_t)rows * 4}},
+              out[3] = {{q_out, (size_t)rows * nq * hd * 2}, {k_pages, pages}, {v_pages, pages}};
+  rc = check_apart(in, 5, out, 3);
+  if (rc) return rc;
   DevInfo* di;
   rc = device_info(&di);
   if (rc) return rc;

@@ -11,9 +11,9 @@ import pytest
 import torch
 
 from oracle import paged as op
-from helpers import np64
+from helpers import np64, oracle_config
 from paged_paths import PATHS
-from test_paged_gpu import api, attn_case, i32, run_attn  # noqa: F401
+from test_paged_gpu import api, attn_case, gen, i32, run_attn, shape_config  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -96,3 +96,43 @@ def test_rising_scores_over_a_prefix_of_its_own(api, P, lens, new):
     ref, size = op.attend(np64(c["q"][rows]), np64(c["k"]), np64(c["v"]), list(range(len(rows) + 1)),
                           [m for _, m in one], [t for t, _ in one], c["ptab"], P, 0)
     assert np.all(np.abs(np64(out[rows]) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -9) * size)
+
+
+@pytest.mark.parametrize("nq,nkv,hd,batch,most,longest", [
+    (8, 2, 64, 4096, 1, 40),       # the most sequences
+    (1, 1, 64, 4096, 256, 256),    # the most rows: 2^20
+    (1024, 64, 64, 3, 2, 300),     # the most heads, 16 to a KV head
+    (64, 64, 128, 2, 130, 200)])
+def test_largest_calls(api, nq, nkv, hd, batch, most, longest):
+    rng = np.random.default_rng(batch)
+    whole = most == 256
+    new = [most if whole else int(rng.integers(0, most + 1)) for _ in range(batch)]
+    lens = [n if whole else n + int(rng.integers(0, longest - most + 1)) for n in new]
+    new[0], lens[0] = most, longest
+    c = attn_case(batch, nq, nkv, hd, 16, 21, lens, new)
+    assert not whole or c["q"].shape[0] == 1 << 20
+    out = run_attn(api, c)
+    assert torch.isfinite(out).all()
+    n = c["start"][-1]
+    close_rows(c, out, 0, sorted({0, n - 1} | {int(r) for r in rng.integers(0, n, 20)}))
+
+
+@pytest.mark.parametrize("nq,nkv,hd", [(160, 20, 128), (320, 40, 64)])
+def test_the_widest_rows(api, nq, nkv, hd):
+    """QKV rows of 25,600 values, the most: append and attention."""
+    cfg = shape_config(nq, nkv, hd)
+    assert cfg.qkv_dim == 25600
+    g, rows, page = gen(1), 5, 16
+    y = torch.randn((rows, cfg.qkv_dim), generator=g, device="cuda")
+    qg, kg = 1 + 0.2 * torch.randn(nq * hd, generator=g, device="cuda"), torch.ones(nkv * hd, device="cuda")
+    k = torch.zeros((2, nkv, page, hd), dtype=torch.bfloat16, device="cuda")
+    v, slots, pos = torch.zeros_like(k), [3, 17, 4, 31, 0], [0, 1, 2, 3, 4]
+    ws = api.zeros_workspace(256)
+    q = api.qk_prep_paged(cfg, True, y, qg, kg, i32(pos), i32(slots), k, v, ws=ws)
+    api.check(ws)
+    rq, rk, rv, qs, ks = op.prep(oracle_config(cfg), np64(y), np64(qg), np64(kg), pos, True)
+    K, V = (np64(t).transpose(0, 2, 1, 3).reshape(-1, nkv, hd)[slots] for t in (k, v))
+    # (the bounds of test_paged_gpu.py; a sum of squares of up to 20,480 terms in a tree)
+    assert np.all(np.abs(np64(q) - rq) <= 2.0 ** -8 * np.abs(rq) + 2.0 ** -18 * qs)
+    assert np.all(np.abs(K - rk) <= 2.0 ** -8 * np.abs(rk) + 2.0 ** -18 * ks)
+    assert np.array_equal(V, np64(torch.from_numpy(rv).to(torch.bfloat16)))

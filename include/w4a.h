@@ -433,8 +433,14 @@ W4A_API int w4a_qk_prep_paged(const W4AConfig* cfg, int full, const float* qkv, 
  * A sequence whose numbers do not fit (n > max_new, n > lens[b], lens[b] beyond
  * the table, rows outside [0, rows]) is skipped, a page id outside the cache
  * makes the outputs that read it meaningless; both are reported by w4a_check.
- * Softmax statistics and sums in fp32, in a fixed order: results are
- * bit-reproducible.
+ * Scores, softmax statistics and sums in fp32, in a fixed order: results are
+ * bit-reproducible.  The softmax weights are rounded to bf16 (2^-8 of each)
+ * before the product with V, as in w4a_attn_prefill; with max_new (or rows) x
+ * query heads per KV head <= 16 the remainders are added, but for a long prefix
+ * that more than 16 such rows share.  So the last bits of a sequence's output
+ * depend on what else is in the call.
+ * The time depends on the tables' width too: the host, which does not know the
+ * lengths, divides the SMs between a long prefix and tables that are 85 % full.
  * ws: device scratch of w4a_attn_shared_workspace_bytes() bytes, its first 256
  * zeroed once (error word); not shared by calls that overlap in time. */
 W4A_API int w4a_attn_shared_workspace_bytes(int rows, int batch, int n_heads, int n_kv_heads, int head_dim, int max_new,

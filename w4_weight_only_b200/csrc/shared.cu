@@ -836,9 +836,13 @@ __global__ void __launch_bounds__(TC_THREADS, 1)
 // four key quarters are joined through the stage of its last tile (one
 // m-tile), or through memory of their own.  The last warp loads, running ahead
 // over segments.  mma.sync, since so few rows would fill a small part of a
-// tcgen05 tile, and memory bounds this kernel all the same: 16 sequences of
-// up to 16,384 positions (600 MB) take 97 us, 6.2 TB/s, one of 65,536 51 us,
-// 5.3 TB/s; its start and end are ~8 us of each.  Up to 16 rows the tensor pipe
+// tcgen05 tile.  Up to 16 rows memory bounds this kernel all the same: 16
+// sequences of up to 16,384 positions (600 MB) take 97 us, 6.2 TB/s, one of 65,536
+// 51 us, 5.3 TB/s; its start and end are ~8 us of each.  With three m-tiles it
+// does not get there: 24 sequences of 5 to 9 rows and up to 9,000 positions take
+// 158 us with pages of 16 (483 MB, 3.1 TB/s) and 149 with pages of 64 (554 MB,
+// 3.7 TB/s): every m-tile reads the K and V fragments for itself, and one CTA an
+// SM has three stages in flight.  Up to 16 rows the tensor pipe
 // has time to spare, and P goes in as two bf16 terms, P and its rounding
 // error, for two products; above rounded to bf16 once.
 template <int HD, int MG>
